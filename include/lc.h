@@ -81,7 +81,9 @@ enum {
 enum {
   LC_FMT_F32 = 0,          /* one FP32 array [n, D] */
   LC_FMT_BF16 = 1,         /* one BF16 array [n, D] */
-  LC_FMT_E4M3_BF16 = 2     /* nope dims E4M3 [n, D - d_r] + RoPE dims BF16 [n, d_r] */
+  LC_FMT_E4M3_BF16 = 2,    /* nope dims E4M3 [n, D - d_r] + RoPE dims BF16 [n, d_r] */
+  LC_FMT_MXFP8 = 3         /* E4M3 codes [n, d] + one E8M0 scale per 32 values [n, d/32]: only
+                              the output of add_rms_norm and the input of w4_proj */
 };
 
 /* Lightning-indexer operand formats. */
@@ -463,6 +465,156 @@ typedef struct lc_out_proj_args {
 
 lc_status lc_grouped_out_proj(const lc_out_proj_args* a, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Operators around a dense attention layer that is served from an 8-bit cache.  The pages
+ * name such layers as what CSA and HCA are measured against ("DeepSeek-V4 论文分析" §八: a
+ * BF16 cache of 8 shared heads of 128 dims); a model keeps them next to CSA / HCA layers.
+ * A step of the layer runs add_rms_norm -> w4_proj (queries, keys, values) -> qk_prep ->
+ * kv8_append -> kv8_attn -> w4_proj (grouped: the output projection).
+ *
+ * add_rms_norm — the residual's addition and RMSNorm with a weight:
+ *   r = x + res (res NULL: r = x);  res_out = r;  y = r / sqrt(mean(r^2) + eps) * w.
+ * r and the sum of squares are FP32; res_out is r rounded to in_fmt, y comes from the
+ * unrounded r.  out_fmt LC_FMT_MXFP8 writes E4M3 codes and, per 32 consecutive values, the
+ * E8M0 scale X (byte e + 127, X = 2^e): the smallest power of two with max |y| <= 448 X over
+ * the block's finite values (e clamped to [-127, 127]; a block of zeros takes 2^0), so no
+ * finite value saturates; infinities become +-448 X, NaN the E4M3 NaN.
+ * res_out may be res or x itself (in place); any other overlap of inputs and outputs is not
+ * allowed.
+ * ------------------------------------------------------------------------------- */
+typedef struct lc_add_rms_norm_args {
+  int64_t n_rows;
+  int32_t d;               /* values per row: multiple of 8 (MXFP8: of 32), <= 16384 */
+  int32_t in_fmt;          /* x, res, res_out: LC_FMT_F32 or LC_FMT_BF16 */
+  const void* x;           /* [n_rows, d] */
+  const void* res;         /* [n_rows, d] or NULL */
+  void* res_out;           /* [n_rows, d] or NULL (not written) */
+  const void* w;           /* [d] or NULL (unit weight) */
+  int32_t w_fmt;           /* LC_FMT_F32 or LC_FMT_BF16 */
+  int32_t out_fmt;         /* LC_FMT_F32, LC_FMT_BF16 or LC_FMT_MXFP8 */
+  void* y;                 /* [n_rows, d] */
+  uint8_t* y_scale;        /* MXFP8: [n_rows, d/32], 4-byte aligned; else unused */
+  float eps;
+  int32_t reserved;
+} lc_add_rms_norm_args;
+
+lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * w4_proj — products of a few rows with 4-bit weights (a decode batch): G groups as in
+ * grouped_out_proj (G = 1: one matrix),
+ *   y[n, g d_g + c] = sum_k x[n, g K + k] W_g[c, k],  0 <= c < d_g,
+ * W in MXFP4 exactly as lc_mxfp4_quantize writes its rows.  x is BF16 or MXFP8.  The products
+ * run on the block-scaled tensor cores (FP32 accumulation) on the caller's weight bytes; a
+ * BF16 row is split there into two E4M3 terms, exact for values down to 2^-15 of the largest
+ * of their 32-value block and within 2^-22 of that largest value below.  A NaN or an infinity
+ * in a BF16 row makes the row's outputs of that group NaN.  Each 64 rows of x read the
+ * weights once: for many rows use a 16-bit product instead.
+ * ------------------------------------------------------------------------------- */
+typedef struct lc_w4_proj_args {
+  int32_t n_q;             /* rows of x */
+  int32_t G;               /* groups */
+  int32_t K;               /* inputs per group: multiple of 32 */
+  int32_t d_g;             /* outputs per group, >= 1 */
+  int32_t in_fmt;          /* LC_FMT_BF16 or LC_FMT_MXFP8 */
+  int32_t out_fmt;         /* LC_FMT_F32 or LC_FMT_BF16 */
+  const void* x;           /* [n_q, G K] BF16, or E4M3 codes */
+  const uint8_t* x_scale;  /* MXFP8: [n_q, G K / 32]; else unused */
+  const uint8_t* w;        /* [G, d_g, K/2] E2M1 codes */
+  const uint8_t* w_scale;  /* [G, d_g, K/32] E8M0, 4-byte aligned */
+  void* y;                 /* [n_q, G d_g] */
+  int32_t* status;         /* optional: LC_DEV_TIMEOUT */
+} lc_w4_proj_args;
+
+lc_status lc_w4_proj(const lc_w4_proj_args* a, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * The 8-bit cache of a dense attention layer: H_kv shared heads, blocks of bt tokens.  Token
+ * t of sequence s is row t % bt of block table[s, t / bt].  Each (block, head) holds bt x D
+ * E4M3 codes and ONE E8M0 scale for the keys, and the same for the values:
+ *   value = code * 2^(scale byte - 127).
+ * Scale exponents run from -32 to 31; bytes outside are read as the nearest of these.
+ * ------------------------------------------------------------------------------- */
+typedef struct lc_kv8_cache {
+  int32_t H_kv;            /* shared heads */
+  int32_t D;               /* dims per head: 64 or 128 */
+  int32_t bt;              /* tokens per block: 16, 32, 64 or 128 */
+  int32_t n_blocks;        /* blocks in the arrays */
+  int32_t table_cols;      /* columns of table */
+  int32_t reserved;
+  uint8_t* k;              /* [n_blocks, H_kv, bt, D] E4M3 */
+  uint8_t* v;              /* [n_blocks, H_kv, bt, D] E4M3 */
+  uint8_t* k_scale;        /* [n_blocks, H_kv] */
+  uint8_t* v_scale;        /* [n_blocks, H_kv] */
+  const int32_t* table;    /* [num_seqs, table_cols] block of each bt tokens; entries outside
+                              [0, n_blocks) are skipped and reported (LC_DEV_BAD_BLOCK) */
+} lc_kv8_cache;
+
+/* kv8_append — the new tokens of each sequence into the cache: rows tok_start[s] ..
+ * tok_start[s+1] - 1 of k and v become tokens pos0[s], pos0[s] + 1, ...  Per (block, head):
+ * e = the smallest exponent in [-32, 31] with max |x| <= 448 2^e over the block's new finite
+ * values.  A block that starts at or after pos0[s] takes the scale 2^e.  One that already
+ * holds tokens (of a position below pos0[s]) takes the larger of its scale and 2^e; when its
+ * scale grows, its older codes are rounded again to the new one (to nearest, ties to even).
+ * Infinities become +-448 2^e, NaN the E4M3 NaN.  Rows of a block past the newest token are
+ * left as they were.  A block that is written must belong to one sequence alone. */
+typedef struct lc_kv8_append_args {
+  lc_kv8_cache cache;
+  int32_t num_seqs;
+  int32_t in_fmt;          /* LC_FMT_F32 or LC_FMT_BF16 */
+  int32_t max_tok;         /* host value: max over s of tok_start[s+1] - tok_start[s] */
+  int32_t reserved;
+  const void* k;           /* [*, H_kv, D] new key rows */
+  const void* v;           /* [*, H_kv, D] new value rows */
+  int64_t k_stride;        /* elements from one token's row to the next (a slice of a fused
+                              projection): multiple of 8, >= H_kv D; 0: H_kv D */
+  int64_t v_stride;
+  const int32_t* tok_start;/* [num_seqs + 1] */
+  const int32_t* pos0;     /* [num_seqs] */
+  int32_t* status;         /* optional: LC_DEV_BAD_BLOCK */
+} lc_kv8_append_args;
+
+lc_status lc_kv8_append(const lc_kv8_append_args* a, void* stream);
+
+/* kv8_attn — attention of H query heads over the 8-bit cache; H / H_kv consecutive heads
+ * share one cache head.  Query i of sequence s sits at p = q_pos0[s] + i and sees the cached
+ * tokens t <= p, t < kv_len[s], and with W > 0 only t > p - W:
+ *   l_t = scale <q_h, k_t>, M = max(sink_h, max l), Z = e^(sink_h - M) + sum e^(l_t - M),
+ *   o = sum e^(l_t - M) v_t / Z, lse = M + ln Z   (sink NULL: no sink term).
+ * A query that sees no token gets o = 0 and lse = sink_h (-inf without a sink).  out and lse
+ * rows past q_start[num_seqs] are left as they were.  A NaN among the keys or values a query
+ * sees makes its outputs NaN; what it does not see never reaches it.
+ * Prefill: any number of queries per sequence.  Decode: one query per sequence (n_q ==
+ * num_seqs, q_start[s] = s).  Both split the keys over CTAs where there are few rows, and then
+ * need a workspace of lc_kv8_attn_workspace_bytes(a, decode) bytes (host fields only). */
+typedef struct lc_kv8_attn_args {
+  lc_kv8_cache cache;      /* read only */
+  int32_t H;               /* query heads: multiple of H_kv */
+  int32_t num_seqs;
+  int32_t n_q;             /* rows of q */
+  int32_t max_q;           /* host value: max over s of its queries */
+  int32_t max_kv;          /* host value: max over s of kv_len[s]; later tokens are not read */
+  int32_t W;               /* window, 0: none */
+  float scale;             /* softmax scale (1/sqrt(D)) */
+  int32_t reserved;
+  const void* q;           /* [n_q, H, D] BF16 */
+  int64_t q_stride;        /* elements from one query's rows to the next: multiple of 8,
+                              >= H D; 0: H D */
+  const int32_t* q_start;  /* [num_seqs + 1] */
+  const int32_t* q_pos0;   /* [num_seqs] position of the first query */
+  const int32_t* kv_len;   /* [num_seqs] cached tokens */
+  const float* sink;       /* [H] or NULL */
+  void* out;               /* [n_q, H, D] BF16 */
+  float* lse;              /* [n_q, H] or NULL */
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* status;         /* optional: LC_DEV_BAD_BLOCK, LC_DEV_TIMEOUT */
+} lc_kv8_attn_args;
+
+lc_status lc_kv8_attn_prefill(const lc_kv8_attn_args* a, void* stream);
+lc_status lc_kv8_attn_decode(const lc_kv8_attn_args* a, void* stream);
+size_t lc_kv8_attn_workspace_bytes(const lc_kv8_attn_args* a, int32_t decode);
+
 /* Library version string (static storage). */
 const char* lc_version(void);
 /* Name of a status code (static storage). */
@@ -470,8 +622,9 @@ const char* lc_status_string(lc_status s);
 /* sizeof of the args structs, for bindings to check their mirrors:
  * 0 lc_rows, 1 lc_dims, 2 lc_batch, 3 lc_qk_prep_args, 4 lc_compress_args,
  * 5 lc_index_args, 6 lc_topk_args, 7 lc_attn_args, 8 lc_index_topk_args,
- * 9 lc_mxfp4_quant_args, 10 lc_index_compress_args, 11 lc_out_proj_args; other values
- * return 0. */
+ * 9 lc_mxfp4_quant_args, 10 lc_index_compress_args, 11 lc_out_proj_args,
+ * 12 lc_add_rms_norm_args, 13 lc_w4_proj_args, 14 lc_kv8_cache, 15 lc_kv8_append_args,
+ * 16 lc_kv8_attn_args; other values return 0. */
 size_t lc_struct_size(int32_t which);
 
 #ifdef __cplusplus

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "liblc.so")
 LC_OK, LC_ERR_ARG, LC_ERR_ALIGN, LC_ERR_UNSUPPORTED, LC_ERR_WORKSPACE, LC_ERR_LAUNCH, LC_ERR_TOO_LARGE = range(7)
 LC_DEV_BAD_INDEX, LC_DEV_WINDOW_RANGE, LC_DEV_BAD_BLOCK, LC_DEV_NONVISIBLE, LC_DEV_TIMEOUT, LC_DEV_RANGE = \
     1, 2, 4, 8, 16, 32
-LC_FMT_F32, LC_FMT_BF16, LC_FMT_E4M3_BF16 = 0, 1, 2
+LC_FMT_F32, LC_FMT_BF16, LC_FMT_E4M3_BF16, LC_FMT_MXFP8 = 0, 1, 2, 3
 LC_IDX_F32, LC_IDX_MXFP4, LC_IDX_MXFP4_QBF16 = 0, 3, 4
 
 
@@ -105,11 +105,43 @@ class AttnArgs(ctypes.Structure):
                 ("n_win_rows", c_int32), ("v_nope", c_int32), ("pdl", c_int32)]
 
 
+class AddRmsNormArgs(ctypes.Structure):
+    _fields_ = [("n_rows", c_int64), ("d", c_int32), ("in_fmt", c_int32), ("x", c_void_p), ("res", c_void_p),
+                ("res_out", c_void_p), ("w", c_void_p), ("w_fmt", c_int32), ("out_fmt", c_int32), ("y", c_void_p),
+                ("y_scale", c_void_p), ("eps", c_float), ("reserved", c_int32)]
+
+
+class W4ProjArgs(ctypes.Structure):
+    _fields_ = [("n_q", c_int32), ("G", c_int32), ("K", c_int32), ("d_g", c_int32), ("in_fmt", c_int32),
+                ("out_fmt", c_int32), ("x", c_void_p), ("x_scale", c_void_p), ("w", c_void_p), ("w_scale", c_void_p),
+                ("y", c_void_p), ("status", c_void_p)]
+
+
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [("H_kv", c_int32), ("D", c_int32), ("bt", c_int32), ("n_blocks", c_int32), ("table_cols", c_int32),
+                ("reserved", c_int32), ("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("table", c_void_p)]
+
+
+class Kv8AppendArgs(ctypes.Structure):
+    _fields_ = [("cache", Kv8Cache), ("num_seqs", c_int32), ("in_fmt", c_int32), ("max_tok", c_int32),
+                ("reserved", c_int32), ("k", c_void_p), ("v", c_void_p), ("k_stride", c_int64), ("v_stride", c_int64),
+                ("tok_start", c_void_p), ("pos0", c_void_p), ("status", c_void_p)]
+
+
+class Kv8AttnArgs(ctypes.Structure):
+    _fields_ = [("cache", Kv8Cache), ("H", c_int32), ("num_seqs", c_int32), ("n_q", c_int32), ("max_q", c_int32),
+                ("max_kv", c_int32), ("W", c_int32), ("scale", c_float), ("reserved", c_int32), ("q", c_void_p),
+                ("q_stride", c_int64), ("q_start", c_void_p), ("q_pos0", c_void_p), ("kv_len", c_void_p),
+                ("sink", c_void_p), ("out", c_void_p), ("lse", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t), ("status", c_void_p)]
+
+
 LC_IMPL_AUTO, LC_IMPL_TC, LC_IMPL_REF = 0, 2, 3
 
 
 STRUCTS = [Rows, Dims, Batch, QkPrepArgs, CompressArgs, IndexArgs, TopkArgs, AttnArgs, IndexTopkArgs, Mxfp4QuantArgs,
-           IndexCompressArgs, OutProjArgs]
+           IndexCompressArgs, OutProjArgs, AddRmsNormArgs, W4ProjArgs, Kv8Cache, Kv8AppendArgs, Kv8AttnArgs]
 
 ENTRY_POINTS = {
     "lc_qk_prep_prefill": QkPrepArgs, "lc_qk_prep_decode": QkPrepArgs,
@@ -124,9 +156,11 @@ ENTRY_POINTS = {
     "lc_csa_sparse_attn_prefill": AttnArgs, "lc_csa_sparse_attn_decode": AttnArgs,
     "lc_hca_attn_prefill": AttnArgs, "lc_hca_attn_decode": AttnArgs,
     "lc_csa_sparse_attn_decode_static": AttnArgs,
+    "lc_add_rms_norm": AddRmsNormArgs, "lc_w4_proj": W4ProjArgs, "lc_kv8_append": Kv8AppendArgs,
+    "lc_kv8_attn_prefill": Kv8AttnArgs, "lc_kv8_attn_decode": Kv8AttnArgs,
 }
 HELPERS = ["lc_csa_sparse_attn_workspace_bytes", "lc_hca_attn_workspace_bytes", "lc_hca_attn_prefill_workspace_bytes",
-           "lc_csa_index_topk_workspace_bytes",
+           "lc_csa_index_topk_workspace_bytes", "lc_kv8_attn_workspace_bytes",
            "lc_version",
            "lc_status_string", "lc_struct_size", "lc_csa_sparse_attn_decode_static_capacity"]
 
@@ -146,6 +180,8 @@ def _load() -> ctypes.CDLL:
         fn.restype = c_size_t
     so.lc_csa_index_topk_workspace_bytes.argtypes = [ctypes.POINTER(IndexTopkArgs), c_int32]
     so.lc_csa_index_topk_workspace_bytes.restype = c_size_t
+    so.lc_kv8_attn_workspace_bytes.argtypes = [ctypes.POINTER(Kv8AttnArgs), c_int32]
+    so.lc_kv8_attn_workspace_bytes.restype = c_size_t
     so.lc_csa_sparse_attn_decode_static_capacity.restype = c_size_t
     so.lc_version.restype = ctypes.c_char_p
     so.lc_status_string.argtypes = [c_int32]
@@ -215,6 +251,10 @@ def lc_hca_attn_prefill_workspace_bytes(args: AttnArgs) -> int:
 
 def lc_csa_index_topk_workspace_bytes(args: IndexTopkArgs, decode: bool) -> int:
     return int(load().lc_csa_index_topk_workspace_bytes(ctypes.byref(args), 1 if decode else 0))
+
+
+def lc_kv8_attn_workspace_bytes(args: Kv8AttnArgs, decode: bool) -> int:
+    return int(load().lc_kv8_attn_workspace_bytes(ctypes.byref(args), 1 if decode else 0))
 
 
 def lc_csa_sparse_attn_decode_static_capacity() -> int:

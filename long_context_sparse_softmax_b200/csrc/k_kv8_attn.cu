@@ -1,0 +1,516 @@
+// kv8_attn: attention over the 8-bit cache (E4M3 codes, one E8M0 scale per block and head).
+//
+// The tokens stream from global memory straight into the registers that the matrix instruction
+// reads; nothing passes through shared memory.  The products are written transposed, keys (then
+// dims) on the 16-row side and 8 query rows on the other, so 8 heads that share a cache head fill
+// the instruction:
+//   S^T[16 keys, 8 rows] = K Q^T      (A = K, B = Q),
+//   O^T[16 dims, 8 rows] += V^T P^T   (A = V^T, B = P).
+// The order of the summed dims is free as long as both operands agree, so a thread's A registers
+// of a key are 16 consecutive bytes of its row (four summed dims per step and thread): whole
+// 32-byte sectors, 16-byte loads.  V^T needs two keys' codes of one dim side by side: the thread
+// that holds dims 16 g .. 16 g + 15 of keys 2t, 2t + 1 interleaves their bytes (one prmt per four)
+// and widens them.  E4M3 is a subset of F16, so widening is exact.
+//
+// Queries are scaled per row by a power of two into F16's range (exact down to 2^-39 of the row's
+// largest value); K's block scale multiplies the logits, V's joins the softmax exponent (see
+// lc_kv8.cuh).  P is rounded to F16 (11 bits); l sums the unrounded weights.  The reference R moves
+// only when a weight would pass 2^8, so the lanes meet once per 16 keys, in a vote.
+//
+// Warps of a CTA take 16-key steps in turn and join through shared memory; the keys of a row
+// tile are split over CTAs, joined by k_kv8_combine.
+#include "lc_e4m3.cuh"
+#include "lc_kv8.cuh"
+
+namespace lc {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kChunk = kKv8MaxSplit;          // keys whose block ids and scales sit in shared memory
+constexpr int kMaxPages = kChunk / 16 + 1;
+constexpr float kHeadroom = 8.f;              // log2 of the largest weight before R moves
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// two E4M3 codes (low 16 bits) -> two F16 values
+__device__ __forceinline__ uint32_t widen2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// A 16-key step of one warp.  k: keys g and g + 8, 16 bytes at 16 t (and at 64 + 16 t for 128 dims);
+// v: keys 2t, 2t + 1, 2t + 8, 2t + 9, D / 8 bytes at (D / 8) g.
+template <int D>
+struct Step {
+  uint32_t k[2][D / 16];
+  uint32_t v[4][D / 32];
+};
+
+}  // namespace
+
+struct Kv8Geom {
+  int g;          // query heads per shared head
+  int row_tiles;  // row tiles per (sequence, shared head)
+  int n_split;    // CTAs per row tile (host's bound); 1: no split
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
+    k_kv8_attn(lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
+  constexpr int kRows = 8 * NT;
+  constexpr int kKS = D / 16;   // summed steps of S
+  constexpr int kMT = D / 16;   // 16-dim tiles of O^T
+  constexpr int kVB = D / 8;    // bytes of V per key and thread
+  __shared__ int s_page[kMaxPages];
+  __shared__ float s_kf[kMaxPages], s_ev[kMaxPages];
+  __shared__ float2 s_ml[kWarps][kRows];
+  __shared__ float s_o[kWarps][kRows][D];
+
+  const lc_kv8_cache& c = a.cache;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  int64_t u = blockIdx.x;
+  const int split = static_cast<int>(u % geo.n_split);
+  u /= geo.n_split;
+  const int rt = static_cast<int>(u % geo.row_tiles);
+  u /= geo.row_tiles;
+  const int h = static_cast<int>(u % c.H_kv);
+  const int s = static_cast<int>(u / c.H_kv);
+
+  const int q0 = __ldg(a.q_start + s);
+  const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
+  const int row0 = rt * kRows;
+  const int64_t all_rows = static_cast<int64_t>(nq) * geo.g;
+  if (nq <= 0 || row0 >= all_rows) return;
+  const int n_row = static_cast<int>(min(static_cast<int64_t>(kRows), all_rows - row0));
+  const int p0 = __ldg(a.q_pos0 + s);
+  const int kv_all = __ldg(a.kv_len + s);
+  const int kv = min(min(kv_all, a.max_kv), c.table_cols * c.bt);
+  if (kv < min(kv_all, a.max_kv) && tid == 0) set_status(a.status, LC_DEV_BAD_BLOCK);
+  const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + (row0 + n_row - 1) / geo.g);
+  const int n = rg.hi - rg.lo16;
+  const int len = geo.n_split > 1 ? kv8_split_len(n) : n;
+  const int n_split = geo.n_split > 1 ? kv8_n_split(n) : 1;
+  if (split >= n_split) return;
+  const int k_begin = rg.lo16 + split * len;
+  const int k_end = min(rg.hi, k_begin + len);
+
+  // queries: B operand, row g8 of each 8-row tile; the row's power of two goes to the logits
+  uint32_t qf[NT][kKS][2];
+  float f_row[NT][2];  // rows 2 t4, 2 t4 + 1: log2(e) scale 2^eq
+  const int64_t q_stride = a.q_stride ? a.q_stride : static_cast<int64_t>(a.H) * D;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = row0 + i * 8 + g8;
+    const bool on = i * 8 + g8 < n_row;
+    uint32_t w[kKS][2];
+    float amax = 0.f;
+    const uint16_t* qr = static_cast<const uint16_t*>(a.q) + (q0 + r / geo.g) * q_stride +
+                         (static_cast<int64_t>(h) * geo.g + r % geo.g) * D;
+#pragma unroll
+    for (int k = 0; k < kKS; ++k) {
+      // dims 16 t + 4 (k % 4) .. + 3, past 64 for the second half
+      uint2 v = make_uint2(0, 0);
+      if (on) v = __ldg(reinterpret_cast<const uint2*>(qr + (k / 4) * 64 + 16 * t4 + 4 * (k % 4)));
+      w[k][0] = v.x;
+      w[k][1] = v.y;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[k][j] << 16)), finite_abs(__uint_as_float(w[k][j] & 0xffff0000u))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // largest value into [2^14, 2^15)
+    const int eq = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100) : 0;
+    const float dn = pow2f(-eq);
+#pragma unroll
+    for (int k = 0; k < kKS; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const __half2 hv = __floats2half2_rn(__uint_as_float(w[k][j] << 16) * dn, __uint_as_float(w[k][j] & 0xffff0000u) * dn);
+        qf[i][k][j] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+    const float f = a.scale * kLog2e * pow2f(eq);
+    f_row[i][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
+    f_row[i][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+  }
+  // visible keys of this thread's rows
+  int r_lo[NT][2], r_hi[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int rr = i * 8 + 2 * t4 + j;
+      const Kv8Range x = kv8_range(kv, a.W, p0 + (row0 + rr) / geo.g, p0 + (row0 + rr) / geo.g);
+      r_lo[i][j] = x.lo;
+      r_hi[i][j] = rr < n_row ? x.hi : 0;
+    }
+  // keys that every row sees: [all_lo, all_hi)
+  const Kv8Range first = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row0 / geo.g);
+  const Kv8Range last = kv8_range(kv, a.W, p0 + (row0 + n_row - 1) / geo.g, p0 + (row0 + n_row - 1) / geo.g);
+  const int all_lo = last.lo, all_hi = first.hi;
+
+  float o[NT][kMT][4];
+  float R[NT][2], l[NT][2];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int m = 0; m < kMT; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][m][j] = 0.f;
+    R[i][0] = R[i][1] = -INFINITY;
+    l[i][0] = l[i][1] = 0.f;
+  }
+
+  bool nan_seen = false;  // NaN value codes replaced in an edge step
+  for (int c0 = k_begin; c0 < k_end; c0 += kChunk) {
+    const int c1 = min(k_end, c0 + kChunk);
+    const int pg0 = c0 / c.bt;
+    const int n_pg = (c1 - 1) / c.bt - pg0 + 1;
+    if (c0 > k_begin) __syncthreads();
+    for (int i = tid; i < n_pg; i += kThreads) {
+      int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + pg0 + i);
+      if (blk < 0 || blk >= c.n_blocks) {
+        blk = -1;
+        set_status(a.status, LC_DEV_BAD_BLOCK);
+      }
+      const int64_t slot = static_cast<int64_t>(blk < 0 ? 0 : blk) * c.H_kv + h;
+      s_page[i] = blk;
+      s_kf[i] = blk < 0 ? 0.f : pow2f(kv8_exp(__ldg(c.k_scale + slot)));
+      s_ev[i] = blk < 0 ? 0.f : static_cast<float>(kv8_exp(__ldg(c.v_scale + slot)));
+    }
+    __syncthreads();
+
+    Step<D> cur, nxt;
+    auto load = [&](int t0, Step<D>& st) {
+      const int pg = t0 < c1 ? s_page[t0 / c.bt - pg0] : -1;
+      if (pg < 0) return;  // never used
+      const int64_t at = ((static_cast<int64_t>(pg) * c.H_kv + h) * c.bt + t0 % c.bt) * D;
+      const uint8_t* kp = c.k + at + g8 * D + 16 * t4;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const uint4 v = ld16(kp + r * 8 * D + x * 64);
+          st.k[r][4 * x] = v.x;
+          st.k[r][4 * x + 1] = v.y;
+          st.k[r][4 * x + 2] = v.z;
+          st.k[r][4 * x + 3] = v.w;
+        }
+      const uint8_t* vp = c.v + at + kVB * g8;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t* p = vp + (2 * t4 + (r & 1) + (r >> 1) * 8) * D;
+        if constexpr (D == 128) {
+          const uint4 v = ld16(p);
+          st.v[r][0] = v.x;
+          st.v[r][1] = v.y;
+          st.v[r][2] = v.z;
+          st.v[r][3] = v.w;
+        } else {
+          const uint2 v = ld8(p);
+          st.v[r][0] = v.x;
+          st.v[r][1] = v.y;
+        }
+      }
+    };
+
+    load(c0 + warp * 16, cur);
+    for (int t0 = c0 + warp * 16; t0 < c1; t0 += 16 * kWarps) {
+      load(t0 + 16 * kWarps, nxt);
+      const int ip = t0 / c.bt - pg0;
+      if (s_page[ip] >= 0) {
+        const float kf = s_kf[ip], ev = s_ev[ip];
+        const float un_ev = pow2f(-static_cast<int>(ev));
+        const bool edge = t0 < all_lo || t0 + 16 > all_hi;
+        float x[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < kKS; ++k) {
+            mma16816(sc, widen2(cur.k[0][k]), widen2(cur.k[1][k]), widen2(cur.k[0][k] >> 16), widen2(cur.k[1][k] >> 16),
+                     qf[i][k][0], qf[i][k][1]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i][j] = fmaf(sc[j], f_row[i][j & 1] * kf, ev);
+        }
+        if (edge) {
+          const int ka = t0 + g8, kb = ka + 8;
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (ka < r_lo[i][j] || ka >= r_hi[i][j]) x[i][j] = -INFINITY;
+              if (kb < r_lo[i][j] || kb >= r_hi[i][j]) x[i][2 + j] = -INFINITY;
+            }
+          // rows of the block that nobody sees may hold anything: their weight 0 must not meet a NaN
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = t0 + 2 * t4 + (r & 1) + (r >> 1) * 8;
+            const bool out = key < rg.lo || key >= rg.hi;
+#pragma unroll
+            for (int q = 0; q < D / 32; ++q) {
+              const uint32_t m = out ? 0xffffffffu : nan_bytes(cur.v[r][q]);
+              nan_seen |= !out && m != 0;
+              cur.v[r][q] &= ~m;
+            }
+          }
+        }
+        bool up = false;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) up |= fmaxf(x[i][j], x[i][2 + j]) > R[i][j] + kHeadroom;
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float m = fmaxf(x[i][j], x[i][2 + j]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              m = fmaxf(m, R[i][j]);
+              const float al = ref_factor(R[i][j], m);
+              R[i][j] = m;
+              l[i][j] *= al;
+#pragma unroll
+              for (int d = 0; d < kMT; ++d) {
+                o[i][d][j] *= al;
+                o[i][d][2 + j] *= al;
+              }
+            }
+        }
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float ra = R[i][0] == -INFINITY ? 0.f : R[i][0], rb = R[i][1] == -INFINITY ? 0.f : R[i][1];
+          const float w0 = ex2(x[i][0] - ra), w1 = ex2(x[i][1] - rb), w2 = ex2(x[i][2] - ra), w3 = ex2(x[i][3] - rb);
+          l[i][0] = fmaf(w0 + w2, un_ev, l[i][0]);
+          l[i][1] = fmaf(w1 + w3, un_ev, l[i][1]);
+          const __half2 ha = __floats2half2_rn(w0, w1), hb = __floats2half2_rn(w2, w3);
+          pf[i][0] = movm(*reinterpret_cast<const uint32_t*>(&ha));
+          pf[i][1] = movm(*reinterpret_cast<const uint32_t*>(&hb));
+        }
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          // bytes 4q .. 4q + 3 of the thread's dims: tiles 2q, 2q + 1
+          const uint32_t lo0 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x5140), lo1 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x7362);
+          const uint32_t hi0 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x5140), hi1 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x7362);
+          const uint32_t a0 = widen2(lo0), a1 = widen2(lo0 >> 16), a2 = widen2(hi0), a3 = widen2(hi0 >> 16);
+          const uint32_t b0 = widen2(lo1), b1 = widen2(lo1 >> 16), b2 = widen2(hi1), b3 = widen2(hi1 >> 16);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            mma16816(o[i][2 * q], a0, a1, a2, a3, pf[i][0], pf[i][1]);
+            mma16816(o[i][2 * q + 1], b0, b1, b2, b3, pf[i][0], pf[i][1]);
+          }
+        }
+      }
+      cur = nxt;
+    }
+  }
+
+  // join the warps
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], 4);
+      l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], 8);
+      l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], 16);
+      const int r = i * 8 + 2 * t4 + j;
+      if (g8 == 0) s_ml[warp][r] = make_float2(R[i][j], l[i][j]);
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+        *reinterpret_cast<float2*>(&s_o[warp][r][kVB * g8 + 2 * m]) = make_float2(o[i][m][j], o[i][m][2 + j]);
+    }
+  const bool nans = __syncthreads_or(nan_seen);
+  for (int i = tid; i < n_row * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    float M = s_ml[0][r].x;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ref_factor(s_ml[w][r].x, M);
+      L = fmaf(s_ml[w][r].y, f, L);
+      const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+    const int rr = row0 + r;
+    if (nans) {
+      // the edge steps that this row sees: below all_lo, and from the step of all_hi on
+      const Kv8Range x = kv8_range(kv, a.W, p0 + rr / geo.g, p0 + rr / geo.g);
+      const int lo = max(x.lo, k_begin), hi = min(x.hi, k_end);
+      const uint32_t m = kv8_value_nans(c, s, h, lo, min(hi, (all_lo + 15) & ~15), d) |
+                         kv8_value_nans(c, s, h, max(lo, all_hi & ~15), hi, d);
+      if (m & 0xffu) acc.x = NAN;
+      if (m & 0xff00u) acc.y = NAN;
+      if (m & 0xff0000u) acc.z = NAN;
+      if (m & 0xff000000u) acc.w = NAN;
+    }
+    const int head = h * geo.g + rr % geo.g;
+    const int64_t orow = static_cast<int64_t>(q0 + rr / geo.g) * a.H + head;
+    if (n_split > 1) {
+      *reinterpret_cast<float4*>(ws_o + (orow * geo.n_split + split) * D + d) = acc;
+      if (d == 0) ws_ml[orow * geo.n_split + split] = make_float2(M, L);
+    } else {
+      float lse;
+      const float f = kv8_finish(M, L, a.sink, head, &lse);
+      const uint32_t w0 = static_cast<uint32_t>(f32_to_bf16_bits(acc.x * f)) |
+                          (static_cast<uint32_t>(f32_to_bf16_bits(acc.y * f)) << 16);
+      const uint32_t w1 = static_cast<uint32_t>(f32_to_bf16_bits(acc.z * f)) |
+                          (static_cast<uint32_t>(f32_to_bf16_bits(acc.w * f)) << 16);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + d) = make_uint2(w0, w1);
+      if (a.lse && d == 0) a.lse[orow] = lse;
+    }
+  }
+}
+
+// Joins the splits of each row: one warp per (query, head), splits in order.
+template <int D>
+__global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo, int rows_per_tile,
+                                                     const float* __restrict__ ws_o, const float2* __restrict__ ws_ml) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t orow = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (orow >= static_cast<int64_t>(a.n_q) * a.H) return;
+  const int q = static_cast<int>(orow / a.H), head = static_cast<int>(orow % a.H);
+  if (q < __ldg(a.q_start) || q >= __ldg(a.q_start + a.num_seqs)) return;
+  const int s = seq_of_query(a.q_start, a.num_seqs, q);
+  const int q0 = __ldg(a.q_start + s), p0 = __ldg(a.q_pos0 + s);
+  const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
+  if (q - q0 >= nq) return;
+  // the range of the row tile that held this row
+  const int rr = (q - q0) * geo.g + head % geo.g;
+  const int row0 = rr / rows_per_tile * rows_per_tile;
+  const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + rows_per_tile, static_cast<int64_t>(nq) * geo.g)) - 1;
+  const int kv = min(min(__ldg(a.kv_len + s), a.max_kv), a.cache.table_cols * a.cache.bt);
+  const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row1 / geo.g);
+  const int n_split = kv8_n_split(rg.hi - rg.lo16);
+  if (n_split <= 1) return;
+  const float2* ml = ws_ml + orow * geo.n_split;
+  float M = -INFINITY;
+  for (int i = lane; i < n_split; i += 32) M = fmaxf(M, ml[i].x);
+  M = warp_max(M);
+  constexpr int kE = D / 32;
+  float acc[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  float L = 0.f;
+  const float* po = ws_o + orow * geo.n_split * D + lane * kE;
+#pragma unroll 4
+  for (int i = 0; i < n_split; ++i) {
+    const float2 x = ml[i];
+    const float f = ref_factor(x.x, M);
+    L = fmaf(x.y, f, L);
+    float v[kE];
+    if constexpr (kE == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * D);
+      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(i) * D);
+      v[0] = t.x; v[1] = t.y;
+    }
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+  }
+  float lse;
+  const float f = kv8_finish(M, L, a.sink, head, &lse);
+  uint32_t w[kE / 2];
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e)
+    w[e] = static_cast<uint32_t>(f32_to_bf16_bits(f == 0.f ? 0.f : acc[2 * e] * f)) |
+           (static_cast<uint32_t>(f32_to_bf16_bits(f == 0.f ? 0.f : acc[2 * e + 1] * f)) << 16);
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + lane * kE);
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) out[e] = w[e];
+  if (a.lse && lane == 0) a.lse[orow] = lse;
+}
+
+namespace {
+
+int row_tile(int g) { return g <= 8 ? 8 : 16; }
+
+// Splits that any row tile of the call can have.
+Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
+  Kv8Geom geo;
+  geo.g = a.H / a.cache.H_kv;
+  const int rt = row_tile(geo.g);
+  geo.row_tiles = static_cast<int>((static_cast<int64_t>(a.max_q) * geo.g + rt - 1) / rt);
+  geo.n_split = 1;
+  if (decode) {
+    int n = a.max_kv;
+    if (a.W > 0 && a.W < n - 16) n = a.W + 16;
+    // the split length is 256 up to 32768 keys and n / 128 (rounded up) above: at most 128 splits
+    // below 2^20 keys, then 8192 keys each
+    geo.n_split = n <= kKv8MinSplit * kKv8Splits ? kv8_n_split(n) : max(kKv8Splits, kv8_n_split(n));
+  }
+  return geo;
+}
+
+size_t align16(size_t n) { return (n + 15) & ~size_t{15}; }
+
+template <int D>
+cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t st) {
+  const int64_t grid = static_cast<int64_t>(geo.n_split) * geo.row_tiles * a.cache.H_kv * a.num_seqs;
+  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const size_t rows = static_cast<size_t>(a.n_q) * a.H;
+  float* ws_o = static_cast<float*>(a.workspace);
+  float2* ws_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align16(rows * geo.n_split * D * 4));
+  if (row_tile(geo.g) == 8) k_kv8_attn<D, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
+  else k_kv8_attn<D, 2><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
+  if (geo.n_split == 1) return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, true, 1, a, geo,
+                   row_tile(geo.g), static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));
+}
+
+}  // namespace
+
+size_t kv8_attn_workspace(const lc_kv8_attn_args& a, bool decode) {
+  const Kv8Geom geo = geometry(a, decode);
+  if (geo.n_split == 1) return 0;
+  const size_t rows = static_cast<size_t>(a.n_q) * a.H;
+  return align16(rows * geo.n_split * a.cache.D * 4) + rows * geo.n_split * sizeof(float2);
+}
+
+cudaError_t launch_kv8_attn(const lc_kv8_attn_args& a, bool decode, cudaStream_t st) {
+  const Kv8Geom geo = geometry(a, decode);
+  return a.cache.D == 128 ? launch<128>(a, geo, st) : launch<64>(a, geo, st);
+}
+
+}  // namespace lc

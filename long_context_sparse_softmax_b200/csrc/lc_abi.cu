@@ -153,6 +153,89 @@ lc_status out_proj(const lc_out_proj_args* a, void* stream) {
   return launched(lc::launch_out_proj(*a, static_cast<cudaStream_t>(stream)));
 }
 
+lc_status add_rms_norm(const lc_add_rms_norm_args* a, void* stream) {
+  if (!a) return LC_ERR_ARG;
+  if (a->n_rows < 0 || a->d < 8 || a->d > 16384 || a->d % 8) return LC_ERR_ARG;
+  if (a->in_fmt != LC_FMT_F32 && a->in_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  if (a->w && a->w_fmt != LC_FMT_F32 && a->w_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  const bool mx = a->out_fmt == LC_FMT_MXFP8;
+  if (!mx && a->out_fmt != LC_FMT_F32 && a->out_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  if (mx && a->d % 32) return LC_ERR_ARG;
+  if (!(a->eps >= 0.f)) return LC_ERR_ARG;
+  if (a->n_rows == 0) return LC_OK;
+  if (a->n_rows > (int64_t{1} << 31) - 1) return LC_ERR_ARG;  // one CTA or more per row
+  if (!a->x || !a->y || (mx && !a->y_scale)) return LC_ERR_ARG;
+  if (!aligned16(a->x) || !aligned16(a->y) || (a->res && !aligned16(a->res)) ||
+      (a->res_out && !aligned16(a->res_out)) || (a->w && !aligned16(a->w)) ||
+      (mx && (reinterpret_cast<uintptr_t>(a->y_scale) & 3u)))
+    return LC_ERR_ALIGN;
+  return launched(lc::launch_add_rms_norm(*a, static_cast<cudaStream_t>(stream)));
+}
+
+lc_status w4_proj(const lc_w4_proj_args* a, void* stream) {
+  if (!a) return LC_ERR_ARG;
+  if (a->n_q < 0 || a->G < 1 || a->d_g < 1 || a->K < 32 || a->K % 32) return LC_ERR_ARG;
+  if (a->out_fmt != LC_FMT_F32 && a->out_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  const bool mx = a->in_fmt == LC_FMT_MXFP8;
+  if (!mx && a->in_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  // launch limits: 2^31 - 1 CTAs in x, 65535 in y
+  const int64_t tiles = static_cast<int64_t>(a->G) * ((static_cast<int64_t>(a->d_g) + 127) / 128);
+  if (tiles > (int64_t{1} << 27) || static_cast<int64_t>(a->G) * a->K > (int64_t{1} << 30) ||
+      (static_cast<int64_t>(a->n_q) + 63) / 64 > 65535)
+    return LC_ERR_UNSUPPORTED;
+  if (a->n_q == 0) return LC_OK;
+  if (!a->x || !a->w || !a->w_scale || !a->y || (mx && !a->x_scale)) return LC_ERR_ARG;
+  if (!aligned16(a->x) || !aligned16(a->w) || !aligned16(a->y) || (reinterpret_cast<uintptr_t>(a->w_scale) & 3u))
+    return LC_ERR_ALIGN;
+  return launched(lc::launch_w4_proj(*a, static_cast<cudaStream_t>(stream)));
+}
+
+// The cache's shape; its pointers too when `need`.
+lc_status check_kv8(const lc_kv8_cache& c, bool need) {
+  if (c.H_kv < 1 || c.n_blocks < 0 || c.table_cols < 0) return LC_ERR_ARG;
+  if ((c.D != 64 && c.D != 128) || (c.bt != 16 && c.bt != 32 && c.bt != 64 && c.bt != 128)) return LC_ERR_UNSUPPORTED;
+  // token positions are 32-bit
+  if (static_cast<int64_t>(c.table_cols) * c.bt > INT32_MAX) return LC_ERR_ARG;
+  if (!need) return LC_OK;
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale || !c.table) return LC_ERR_ARG;
+  if (!aligned16(c.k) || !aligned16(c.v)) return LC_ERR_ALIGN;
+  return LC_OK;
+}
+
+// A row stride in elements: 0 (dense) or a multiple of 8 that holds a row.
+bool bad_stride(int64_t stride, int64_t row) { return stride != 0 && (stride < row || stride % 8); }
+
+lc_status kv8_append(const lc_kv8_append_args* a, void* stream) {
+  if (!a) return LC_ERR_ARG;
+  LC_TRY(check_kv8(a->cache, false));
+  if (a->in_fmt != LC_FMT_F32 && a->in_fmt != LC_FMT_BF16) return LC_ERR_ARG;
+  if (a->num_seqs < 0 || a->max_tok < 0) return LC_ERR_ARG;
+  const int64_t row = static_cast<int64_t>(a->cache.H_kv) * a->cache.D;
+  if (bad_stride(a->k_stride, row) || bad_stride(a->v_stride, row)) return LC_ERR_ARG;
+  if (a->num_seqs == 0 || a->max_tok == 0) return LC_OK;
+  LC_TRY(check_kv8(a->cache, true));
+  if (!a->k || !a->v || !a->tok_start || !a->pos0) return LC_ERR_ARG;
+  if (!aligned16(a->k) || !aligned16(a->v)) return LC_ERR_ALIGN;
+  return launched(lc::launch_kv8_append(*a, static_cast<cudaStream_t>(stream)));
+}
+
+lc_status kv8_attn(const lc_kv8_attn_args* a, void* stream, bool decode) {
+  if (!a) return LC_ERR_ARG;
+  LC_TRY(check_kv8(a->cache, false));
+  if (a->H < 1 || a->H % a->cache.H_kv || a->num_seqs < 0 || a->n_q < 0 || a->max_q < 0 || a->max_kv < 0 || a->W < 0)
+    return LC_ERR_ARG;
+  if (bad_stride(a->q_stride, static_cast<int64_t>(a->H) * a->cache.D)) return LC_ERR_ARG;
+  if (decode && (a->n_q != a->num_seqs || a->max_q > 1)) return LC_ERR_ARG;
+  if (a->n_q == 0 || a->num_seqs == 0 || a->max_q == 0) return LC_OK;
+  LC_TRY(check_kv8(a->cache, a->max_kv > 0));
+  if (!a->q || !a->q_start || !a->q_pos0 || !a->kv_len || !a->out) return LC_ERR_ARG;
+  if (!aligned16(a->q) || !aligned16(a->out)) return LC_ERR_ALIGN;
+  const size_t need = lc::kv8_attn_workspace(*a, decode);
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return LC_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(a->workspace)) return LC_ERR_ALIGN;
+  return launched(lc::launch_kv8_attn(*a, decode, static_cast<cudaStream_t>(stream)));
+}
+
 lc_status index_scores(const lc_index_args* a, void* stream, bool decode) {
   LC_TRY(check_index(a, decode, true));
   if (a->n_q == 0 || a->max_ent == 0) return LC_OK;
@@ -230,6 +313,18 @@ lc_status lc_csa_index_scores_decode(const lc_index_args* a, void* stream) { ret
 
 lc_status lc_mxfp4_quantize(const lc_mxfp4_quant_args* a, void* stream) { return mxfp4_quantize(a, stream); }
 lc_status lc_grouped_out_proj(const lc_out_proj_args* a, void* stream) { return out_proj(a, stream); }
+lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream) { return add_rms_norm(a, stream); }
+lc_status lc_w4_proj(const lc_w4_proj_args* a, void* stream) { return w4_proj(a, stream); }
+lc_status lc_kv8_append(const lc_kv8_append_args* a, void* stream) { return kv8_append(a, stream); }
+lc_status lc_kv8_attn_prefill(const lc_kv8_attn_args* a, void* stream) { return kv8_attn(a, stream, false); }
+lc_status lc_kv8_attn_decode(const lc_kv8_attn_args* a, void* stream) { return kv8_attn(a, stream, true); }
+// 0 for arguments that the calls refuse
+size_t lc_kv8_attn_workspace_bytes(const lc_kv8_attn_args* a, int32_t decode) {
+  if (!a || check_kv8(a->cache, false) != LC_OK || a->H < 1 || a->H % a->cache.H_kv || a->n_q <= 0 ||
+      a->num_seqs <= 0 || a->max_q <= 0 || a->max_kv <= 0)
+    return 0;
+  return lc::kv8_attn_workspace(*a, decode != 0);
+}
 lc_status lc_csa_index_compress_prefill(const lc_index_compress_args* a, void* stream) { return index_compress(a, stream); }
 lc_status lc_csa_index_compress_decode(const lc_index_compress_args* a, void* stream) { return index_compress(a, stream); }
 
@@ -289,6 +384,11 @@ size_t lc_struct_size(int32_t which) {
     case 9: return sizeof(lc_mxfp4_quant_args);
     case 10: return sizeof(lc_index_compress_args);
     case 11: return sizeof(lc_out_proj_args);
+    case 12: return sizeof(lc_add_rms_norm_args);
+    case 13: return sizeof(lc_w4_proj_args);
+    case 14: return sizeof(lc_kv8_cache);
+    case 15: return sizeof(lc_kv8_append_args);
+    case 16: return sizeof(lc_kv8_attn_args);
     default: return 0;
   }
 }

@@ -47,6 +47,11 @@ cudaError_t launch_compress(const lc_compress_args& a, bool per_cta, cudaStream_
 cudaError_t launch_mxfp4_quantize(const lc_mxfp4_quant_args& a, cudaStream_t st);
 cudaError_t launch_index_compress(const lc_index_compress_args& a, cudaStream_t st);
 cudaError_t launch_out_proj(const lc_out_proj_args& a, cudaStream_t st);
+cudaError_t launch_add_rms_norm(const lc_add_rms_norm_args& a, cudaStream_t st);
+cudaError_t launch_w4_proj(const lc_w4_proj_args& a, cudaStream_t st);
+cudaError_t launch_kv8_append(const lc_kv8_append_args& a, cudaStream_t st);
+size_t kv8_attn_workspace(const lc_kv8_attn_args& a, bool decode);
+cudaError_t launch_kv8_attn(const lc_kv8_attn_args& a, bool decode, cudaStream_t st);
 cudaError_t launch_index_scores(const lc_index_args& a, bool decode, cudaStream_t st);
 cudaError_t launch_topk(const lc_topk_args& a, bool decode, cudaStream_t st);
 // idx[q, :] = -1 and count[q] = 0 for every query

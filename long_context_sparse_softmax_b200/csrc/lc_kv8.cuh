@@ -1,0 +1,95 @@
+// What the kernels that read the 8-bit cache share: the key range of a tile of query rows, its
+// splits, the scale bytes, and the joining of partial softmax results.
+//
+// A partial result over some keys is (O, R, l): with x_t = log2(e) scale <q, k_t> and value
+// exponents ev_t (the value of token t is code_t 2^ev_t),
+//   w_t = 2^(x_t + ev_t - R),  O = sum w_t code_t,  l = sum w_t 2^-ev_t,
+// so o = O / l and lse = ln 2 (R + log2 l).  The reference R follows the largest x_t + ev_t, not
+// the largest logit: the weights that multiply the codes then stay in F16's range whatever the
+// blocks' scales are.  Exponents within [-32, 31] keep l in FP32's range.
+#pragma once
+
+#include "lc_internal.h"
+#include "lc_ptx.cuh"
+
+namespace lc {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kKv8EMin = -32, kKv8EMax = 31;
+
+__device__ __forceinline__ int kv8_exp(uint8_t byte) { return min(max(static_cast<int>(byte) - 127, kKv8EMin), kKv8EMax); }
+
+// 2^(a - b) for references that may both be the same infinity
+__device__ __forceinline__ float ref_factor(float a, float b) { return a == b ? 1.f : ex2(a - b); }
+
+// Keys that the rows [row0, row0 + n_row) of one sequence and shared head can see: [lo, hi); row r
+// is query r / g.  lo16 is lo rounded down to 16 (a 16-key step lies in one block).
+struct Kv8Range {
+  int lo, hi, lo16;
+};
+__device__ __forceinline__ Kv8Range kv8_range(int kv, int W, int p_first, int p_last) {
+  Kv8Range r;
+  r.hi = p_last < kv - 1 ? p_last + 1 : kv;
+  r.lo = W > 0 ? max(0, p_first - (W - 1)) : 0;
+  r.lo16 = r.lo & ~15;
+  if (r.hi <= r.lo) r.hi = r.lo16;
+  return r;
+}
+
+// Split of n keys over CTAs: `len` keys each.  A function of the row's own key count alone, so a
+// sequence's result does not depend on the batch it is in.
+constexpr int kKv8MinSplit = 256, kKv8MaxSplit = 8192, kKv8Splits = 128;
+__host__ __device__ __forceinline__ int kv8_split_len(int n) {
+  const int want = ((n + kKv8Splits - 1) / kKv8Splits + 63) / 64 * 64;
+  return want < kKv8MinSplit ? kKv8MinSplit : want > kKv8MaxSplit ? kKv8MaxSplit : want;
+}
+__host__ __device__ __forceinline__ int kv8_n_split(int n) {
+  const int len = kv8_split_len(n);
+  return n <= len ? 1 : static_cast<int>((static_cast<int64_t>(n) + len - 1) / len);
+}
+
+// A query's weight on a key it does not see is 0, but 0 times the E4M3 NaN is a NaN.  In the steps
+// where rows of a tile see different keys the kernels replace NaN value codes by 0 (nan_bytes) and
+// note it; the rows that do see such a code are then found by reading the codes again (rare).
+
+// 0xff in each byte of v that holds an E4M3 NaN
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t v) {
+  const uint32_t m = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return m | (m - (m >> 7));
+}
+// which of the value codes of dims d .. d + 3 are NaN for some token of [lo, hi): bytes 0xff
+__device__ __forceinline__ uint32_t kv8_value_nans(const lc_kv8_cache& c, int s, int h, int lo, int hi, int d) {
+  uint32_t m = 0;
+  for (int t = lo; t < hi; ++t) {
+    const int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + t / c.bt);
+    if (blk < 0 || blk >= c.n_blocks) continue;
+    m |= nan_bytes(__ldg(reinterpret_cast<const uint32_t*>(
+        c.v + ((static_cast<int64_t>(blk) * c.H_kv + h) * c.bt + t % c.bt) * c.D + d)));
+  }
+  return m;
+}
+
+// The output of one row from its joined partial result: the factor on O, and lse.
+__device__ __forceinline__ float kv8_finish(float R, float l, const float* sink, int head, float* lse) {
+  if (!sink) {
+    if (R == -INFINITY && l == 0.f) {
+      *lse = -INFINITY;
+      return 0.f;
+    }
+    *lse = R * kLn2 + logf(l);
+    return 1.f / l;
+  }
+  const float s2 = __ldg(sink + head) * kLog2e;
+  if (R == -INFINITY && l == 0.f) {
+    *lse = __ldg(sink + head);
+    return 0.f;
+  }
+  const float M = fmaxf(R, s2);
+  const float fr = ref_factor(R, M);
+  const float Z = l * fr + ref_factor(s2, M);
+  *lse = M * kLn2 + logf(Z);
+  return fr / Z;
+}
+
+}  // namespace lc
