@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "liblc.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 SOURCES = ["lc_abi.cu", "k_prep.cu", "k_index.cu", "k_topk.cu", "k_attn.cu", "k_attn_combine.cu", "k_index_tc.cu", "k_attn_tc.cu", "k_attn_tc8.cu", "k_quant.cu", "k_outproj.cu", "k_norm.cu", "k_w4.cu",
-           "k_kv8_append.cu", "k_kv8_attn.cu", "lc_noalloc.cu"]
+           "k_kv8_append.cu", "k_kv8_attn.cu", "k_kv8_attn_tc.cu", "lc_noalloc.cu"]
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",

@@ -74,12 +74,6 @@ struct Step {
 
 }  // namespace
 
-struct Kv8Geom {
-  int g;          // query heads per shared head
-  int row_tiles;  // row tiles per (sequence, shared head)
-  int n_split;    // CTAs per row tile (host's bound); 1: no split
-};
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     k_kv8_attn(lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
@@ -401,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 
 // Joins the splits of each row: one warp per (query, head), splits in order.
 template <int D>
-__global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo, int rows_per_tile,
+__global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo,
                                                      const float* __restrict__ ws_o, const float2* __restrict__ ws_ml) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -415,11 +409,11 @@ __global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom
   if (q - q0 >= nq) return;
   // the range of the row tile that held this row
   const int rr = (q - q0) * geo.g + head % geo.g;
-  const int row0 = rr / rows_per_tile * rows_per_tile;
-  const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + rows_per_tile, static_cast<int64_t>(nq) * geo.g)) - 1;
+  const int row0 = rr / geo.rows * geo.rows;
+  const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + geo.rows, static_cast<int64_t>(nq) * geo.g)) - 1;
   const int kv = min(min(__ldg(a.kv_len + s), a.max_kv), a.cache.table_cols * a.cache.bt);
   const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row1 / geo.g);
-  const int n_split = kv8_n_split(rg.hi - rg.lo16);
+  const int n_split = geo.tc ? geo.n_split : kv8_n_split(rg.hi - rg.lo16);
   if (n_split <= 1) return;
   const float2* ml = ws_ml + orow * geo.n_split;
   float M = -INFINITY;
@@ -434,6 +428,7 @@ __global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom
 #pragma unroll 4
   for (int i = 0; i < n_split; ++i) {
     const float2 x = ml[i];
+    if (x.x == -INFINITY && x.y == 0.f) continue;  // saw no key
     const float f = ref_factor(x.x, M);
     L = fmaf(x.y, f, L);
     float v[kE];
@@ -462,18 +457,26 @@ __global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom
 
 namespace {
 
-int row_tile(int g) { return g <= 8 ? 8 : 16; }
+// From this many rows per (sequence, shared head) on, a call takes the tensor-memory kernel
+constexpr int kTcRows = 64;
 
 // Splits that any row tile of the call can have.
 Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
   Kv8Geom geo;
   geo.g = a.H / a.cache.H_kv;
-  const int rt = row_tile(geo.g);
-  geo.row_tiles = static_cast<int>((static_cast<int64_t>(a.max_q) * geo.g + rt - 1) / rt);
+  const int64_t all = static_cast<int64_t>(a.max_q) * geo.g;
+  geo.tc = !decode && all >= kTcRows;
+  geo.rows = geo.tc ? 256 : geo.g <= 8 ? 8 : 16;
+  geo.row_tiles = static_cast<int>((all + geo.rows - 1) / geo.rows);
   geo.n_split = 1;
-  if (decode) {
-    int n = a.max_kv;
-    if (a.W > 0 && a.W < n - 16) n = a.W + 16;
+  int n = a.max_kv;
+  if (a.W > 0 && a.W + a.max_q - 1 < n - 16) n = a.W + a.max_q - 1 + 16;
+  if (geo.tc) {
+    // fewer CTAs than multiprocessors: split the keys, at least 4 tiles of 128 each
+    const int64_t ctas = static_cast<int64_t>(geo.row_tiles) * a.cache.H_kv * a.num_seqs;
+    const int64_t fill = sm_count() / ctas;
+    geo.n_split = static_cast<int>(max(int64_t{1}, min(fill, static_cast<int64_t>(n) / 512)));
+  } else {
     // the split length is 256 up to 32768 keys and n / 128 (rounded up) above: at most 128 splits
     // below 2^20 keys, then 8192 keys each
     geo.n_split = n <= kKv8MinSplit * kKv8Splits ? kv8_n_split(n) : max(kKv8Splits, kv8_n_split(n));
@@ -490,13 +493,16 @@ cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t s
   const size_t rows = static_cast<size_t>(a.n_q) * a.H;
   float* ws_o = static_cast<float*>(a.workspace);
   float2* ws_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align16(rows * geo.n_split * D * 4));
-  if (row_tile(geo.g) == 8) k_kv8_attn<D, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
+  if (geo.tc) {
+    const cudaError_t e = launch_kv8_attn_tc(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st);
+    if (e != cudaSuccess) return e;
+  } else if (geo.rows == 8) k_kv8_attn<D, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
   else k_kv8_attn<D, 2><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
   if (geo.n_split == 1) return cudaGetLastError();
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, true, 1, a, geo,
-                   row_tile(geo.g), static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));
+                   static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));
 }
 
 }  // namespace

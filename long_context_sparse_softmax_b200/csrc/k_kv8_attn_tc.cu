@@ -1,0 +1,521 @@
+// kv8_attn for many query rows (prefill) on the 5th-generation tensor cores (tcgen05, F16 operands,
+// FP32 accumulators in tensor memory).  The same arithmetic as k_kv8_attn.cu: see lc_kv8.cuh.
+//
+// A CTA holds 256 rows of one sequence and shared head (row r: query r / g, head r % g of the
+// group) as two tiles of 128 rows that share every key tile of 128 tokens:
+//   S_i = Q_i K^T   M = 128 rows, N = 128 keys, both K-major in shared memory;
+//   P_i             F16 weights, written over S_i's columns of tensor memory;
+//   O_i += P_i V    A = P_i in tensor memory, B = V (keys x dims, dims contiguous: MN-major).
+// The codes are widened to F16 (exact) once per CTA, so 256 rows share that work and the row's
+// softmax keeps the precision that it has with few rows.  While one row tile's softmax runs, the
+// tensor core works on the other's products.
+//
+// Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row (its sums need no shuffles).
+// Warps 8-11: fetch codes into registers a tile ahead, widen them into the two-stage rings of K
+// and V.  Warps 12 and 13: lane 0 issues the products of row tile 0 and 1.
+// (Warps 14 and 15 only complete their warpgroup.)  Registers, a thread: 192 for softmax, 96 to
+// widen, 32 to issue: 256 * 192 + 128 * 96 + 128 * 32 = 512 * 128, what the CTA was launched with.
+// A softmax thread computes its tile's weights with the reference R it has; only when one would
+// pass 2^8 does R move, O is rescaled in tensor memory and the weights are computed again (the
+// first tile, and rarely after it).  Tiles whose keys every row sees skip the mask.
+// Every wait on an mbarrier is bounded (LC_DEV_TIMEOUT).
+#include "lc_e4m3.cuh"
+#include "lc_kv8.cuh"
+
+namespace lc {
+
+namespace {
+
+constexpr int kTK = 128;                 // keys per tile
+constexpr int kRT = 128;                 // rows per row tile
+constexpr int kThreads = 512;
+constexpr float kHeadroom = 8.f;
+constexpr long kSpin = 1L << 26;
+constexpr uint32_t kColO = 256;          // S_i at 128 i, O_i at 256 + 128 i
+constexpr int kHalf = kTK * 128;         // bytes of 128 rows x 64 F16 values (SWIZZLE_128B)
+
+struct Bars {
+  uint64_t qfull[2];   // Q_i in shared memory (128 arrivals)
+  uint64_t kfull[2], vfull[2];    // stage written (128)
+  uint64_t kempty[2], vempty[2];  // stage read by every row tile (commits)
+  uint64_t sfull[2];   // S_i computed (commit)
+  uint64_t pfull[2];   // P_i written, O_i rescaled (128)
+  uint64_t ofull[2];   // O_i updated (commit)
+};
+
+__device__ __forceinline__ uint32_t widen2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// D += A B with A (128 rows x 16 F16 values) in tensor memory
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
+// a shared-memory load that stays where it is written: hoisted, the scales of a tile's eight key
+// groups would hold 32 registers
+__device__ __forceinline__ float4 ld_shared4(const float4* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(su32(p)) : "memory");
+  return v;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// offset of chunk j (8 values) of half hf of row r in a tile of 128 rows
+__device__ __forceinline__ uint32_t tile_off(int r, int hf, int j) { return hf * kHalf + sw128_off(r, j); }
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return 6 * static_cast<size_t>(kHalf) * (D / 64) + 1024;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv8_attn_tc(lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
+  constexpr int kTile = kHalf * (D / 64);  // bytes of a 128 x D F16 tile
+  constexpr int kPR = D / 16;              // 16-code pieces per row
+  constexpr int kIt = kTK * kPR / 128;     // pieces per converter thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* Qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Ks = Qs + 2 * kTile;
+  uint8_t* Vs = Ks + 2 * kTile;
+  __shared__ float4 s_sc[4][8];  // per 16 keys of a tile: 2^ek, ev, 2^-ev (ring of 4 tiles)
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_nan;
+  __shared__ __align__(8) Bars bars;
+
+  const lc_kv8_cache& c = a.cache;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int64_t u = blockIdx.x;
+  const int split = static_cast<int>(u % geo.n_split);
+  u /= geo.n_split;
+  const int h = static_cast<int>(u % c.H_kv);
+  u /= c.H_kv;
+  const int s = static_cast<int>(u % a.num_seqs);
+  // the last rows of a sequence see the most keys: they start first
+  const int rt = geo.row_tiles - 1 - static_cast<int>(u / a.num_seqs);
+
+  const int q0 = __ldg(a.q_start + s);
+  const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
+  const int64_t row0 = static_cast<int64_t>(rt) * (2 * kRT);
+  const int64_t all_rows = static_cast<int64_t>(nq) * geo.g;
+  if (nq <= 0 || row0 >= all_rows) return;
+  const int n_row = static_cast<int>(min(static_cast<int64_t>(2 * kRT), all_rows - row0));
+  const int n_act = n_row > kRT ? 2 : 1;
+  const int p0 = __ldg(a.q_pos0 + s);
+  const int kv_all = __ldg(a.kv_len + s);
+  const int kv = min(min(kv_all, a.max_kv), c.table_cols * c.bt);
+  if (kv < min(kv_all, a.max_kv) && tid == 0) set_status(a.status, LC_DEV_BAD_BLOCK);
+  auto pos = [&](int r) { return p0 + static_cast<int>((row0 + r) / geo.g); };
+  const Kv8Range rg = kv8_range(kv, a.W, pos(0), pos(n_row - 1));
+  const int kb0 = rg.lo16 & ~(kTK - 1);
+  const int all_tiles = rg.hi > kb0 ? (rg.hi - kb0 + kTK - 1) / kTK : 0;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / geo.n_split);
+  const int n_tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / geo.n_split) - tile0;
+  const int k0 = kb0 + tile0 * kTK;                      // first key of the CTA
+  const int k_end = min(rg.hi, k0 + n_tiles * kTK);
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const uint32_t addr = su32(bar);
+    for (long it = 0; it < kSpin; ++it) {
+      if (mbar_test(addr, parity)) return true;
+      if ((it & 1023) == 1023 && *reinterpret_cast<volatile int*>(&s_abort)) return false;
+    }
+    set_status(a.status, LC_DEV_TIMEOUT);
+    atomicExch(&s_abort, 1);
+    return false;
+  };
+
+  if (warp == 12) tmem_alloc(su32(&s_tmem), 512);
+  if (tid == 0) {
+    s_abort = s_nan = 0;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(su32(&bars.qfull[i]), 128);
+      mbar_init(su32(&bars.kfull[i]), 128);
+      mbar_init(su32(&bars.vfull[i]), 128);
+      mbar_init(su32(&bars.kempty[i]), n_act);
+      mbar_init(su32(&bars.vempty[i]), n_act);
+      mbar_init(su32(&bars.sfull[i]), 1);
+      mbar_init(su32(&bars.pfull[i]), 128);
+      mbar_init(su32(&bars.ofull[i]), 1);
+    }
+    fence_mbar_init();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tm = s_tmem;
+
+  const int i = warp < 8 ? warp >> 2 : warp - 12;  // row tile of a softmax or issuing warp
+  const int r = tid & 255;                         // softmax: row of the CTA
+  float R = -INFINITY, l = 0.f;
+  bool good = true;
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+
+  if (warp < 8) {
+    regs_inc<192>();
+    if (i < n_act) {
+      // ---------------- Q: the row, scaled by a power of two into F16's range (k_kv8_attn.cu)
+      float f_row;
+      {
+        const int64_t q_stride = a.q_stride ? a.q_stride : static_cast<int64_t>(a.H) * D;
+        const int64_t rr = row0 + r;
+        const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (q0 + rr / geo.g) * q_stride +
+                                                         (static_cast<int64_t>(h) * geo.g + rr % geo.g) * D);
+        uint4 v[D / 8];
+        float amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) v[k] = r < n_row ? __ldg(qr + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[j] << 16)), finite_abs(__uint_as_float(w[j] & 0xffff0000u))));
+        }
+        const int eq = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100) : 0;
+        const float dn = pow2f(-eq);
+        f_row = a.scale * kLog2e * pow2f(eq);
+        uint8_t* qt = Qs + i * kTile;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 hv = __floats2half2_rn(__uint_as_float(w[j] << 16) * dn, __uint_as_float(w[j] & 0xffff0000u) * dn);
+            o[j] = *reinterpret_cast<const uint32_t*>(&hv);
+          }
+          *reinterpret_cast<uint4*>(qt + tile_off(r & (kRT - 1), k / 8, k % 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        fence_async_smem();
+        mbar_arrive(su32(&bars.qfull[i]));
+      }
+      // visible keys of the row, and those that every row of the tile sees
+      const Kv8Range me = kv8_range(kv, a.W, pos(r), pos(r));
+      const int r_lo = me.lo, r_hi = r < n_row ? me.hi : 0;
+      const int last_r = min(n_row, (i + 1) * kRT) - 1;
+      const int all_hi = kv8_range(kv, a.W, pos(i * kRT), pos(i * kRT)).hi;
+      const int all_lo = kv8_range(kv, a.W, pos(last_r), pos(last_r)).lo;
+      const uint32_t ts = tm + lane_off + i * kTK, to = tm + lane_off + kColO + i * 128;
+
+      for (int t = 0; t < n_tiles; ++t) {
+        const int t0 = k0 + t * kTK;
+        const bool edge = t0 < all_lo || t0 + kTK > all_hi;
+        const bool ok = wait(&bars.sfull[i], t & 1) && wait(&bars.kfull[t & 1], (t >> 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          good = false;
+          break;
+        }
+        fence_after();
+        uint32_t pk[kTK / 2];
+        float ls = 0.f, al = 1.f;
+        bool first = true, again;
+        do {
+          const float Ru = R == -INFINITY ? 0.f : R;
+          float ymax = -INFINITY;
+          ls = 0.f;
+          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the tile
+          asm volatile("" : "+r"(d_lo), "+r"(d_hi));  // keep their comparisons inside the loop
+          uint32_t sv[2][16];
+          tmem_ld16(ts, sv[0]);
+#pragma unroll
+          for (int g = 0; g < kTK / 16; ++g) {
+            tmem_wait_ld();
+            if (g + 1 < kTK / 16) tmem_ld16(ts + (g + 1) * 16, sv[(g + 1) & 1]);
+            const float4 sc = ld_shared4(&s_sc[t & 3][g]);
+            const float fk = f_row * sc.x, off = sc.y - Ru;
+            float y[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = fmaf(__uint_as_float(sv[g & 1][j]), fk, off);
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (g * 16 + j < d_lo || g * 16 + j >= d_hi) y[j] = -INFINITY;
+              }
+            }
+            float gs = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              ymax = fmaxf(ymax, fmaxf(y[j], y[j + 1]));
+              const float w0 = ex2(y[j]), w1 = ex2(y[j + 1]);
+              gs += w0 + w1;
+              const __half2 hv = __floats2half2_rn(w0, w1);
+              pk[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            ls = fmaf(gs, sc.z, ls);
+          }
+          const bool need = first && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
+          again = __any_sync(0xffffffffu, need);
+          first = false;
+          if (need) {
+            // the reference moves: weigh the tile again
+            al = ref_factor(R, Ru + ymax);
+            R = Ru + ymax;
+          }
+        } while (again);
+        if (__any_sync(0xffffffffu, al != 1.f) && t > 0) {
+          if (!__all_sync(0xffffffffu, wait(&bars.ofull[i], (t - 1) & 1))) {
+            good = false;
+            break;
+          }
+          fence_after();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            uint32_t ov[16];
+            tmem_ld16(to + d, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * al);
+            tmem_st16(to + d, ov);
+          }
+        }
+        l = fmaf(l, al, ls);
+        uint32_t half[32];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) half[j] = pk[x * 32 + j];
+          tmem_st32(ts + x * 32, half);
+        }
+        tmem_wait_st();
+        fence_before();
+        mbar_arrive(su32(&bars.pfull[i]));
+      }
+      if (good && n_tiles > 0) good = __all_sync(0xffffffffu, wait(&bars.ofull[i], (n_tiles - 1) & 1));
+    }
+    named_bar(1, kThreads);
+    // ---------------- output: a thread per row
+    if (i < n_act) {
+      fence_after();
+      const int64_t rr = row0 + r;
+      const int head = h * geo.g + static_cast<int>(rr % geo.g);
+      const int64_t orow = static_cast<int64_t>(q0 + rr / geo.g) * a.H + head;
+      const bool store = good && r < n_row;
+      const int p = pos(r);
+      float lse = 0.f, f = 1.f;
+      if (geo.n_split == 1) {
+        f = store ? kv8_finish(R, l, a.sink, head, &lse) : 0.f;
+        if (store && a.lse) a.lse[orow] = lse;
+      } else if (store) {
+        ws_ml[orow * geo.n_split + split] = make_float2(R, l);
+      }
+  #pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t ov[32];
+        if (n_tiles > 0) {
+          tmem_ld32(tm + lane_off + kColO + i * 128 + d, ov);
+          tmem_wait_ld();
+        } else {
+  #pragma unroll
+          for (int j = 0; j < 32; ++j) ov[j] = 0;
+        }
+        if (s_nan && store) {
+          // value codes that were replaced: those of the row's keys make its outputs NaN
+          const Kv8Range me = kv8_range(kv, a.W, p, p);
+  #pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const uint32_t m = kv8_value_nans(c, s, h, max(me.lo, k0), min(me.hi, k_end), d + j);
+  #pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if (m >> (8 * b) & 0xffu) ov[j + b] = 0x7fffffffu;
+          }
+        }
+        if (!store) continue;
+        if (geo.n_split > 1) {
+          float* o = ws_o + (orow * geo.n_split + split) * D + d;
+  #pragma unroll
+          for (int j = 0; j < 32; j += 4) *reinterpret_cast<uint4*>(o + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(a.out) + orow * D + d;
+          uint32_t w[16];
+  #pragma unroll
+          for (int j = 0; j < 16; ++j)
+            w[j] = static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(ov[2 * j]) * f)) |
+                   (static_cast<uint32_t>(f32_to_bf16_bits(__uint_as_float(ov[2 * j + 1]) * f)) << 16);
+  #pragma unroll
+          for (int j = 0; j < 16; j += 4) *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        }
+      }
+      fence_before();
+    }
+  } else if (warp < 12) {
+    // ---------------- codes -> F16 tiles
+    regs_dec<96>();
+    const int ct = tid - 256, cw = warp - 8;
+    const int piece = ct % kPR, rsub = ct / kPR;  // rows rsub + it * (128 / kPR)
+    constexpr int kRStep = 128 / kPR;             // 16 (D = 128) or 32 (D = 64)
+    const int all_lo = kv8_range(kv, a.W, pos(n_row - 1), pos(n_row - 1)).lo;  // keys that every row sees
+    const int all_hi = kv8_range(kv, a.W, pos(0), pos(0)).hi;
+    bool nan_seen = false, ok = true;
+    // block of the tile's 16-key group lane % 8
+    auto page = [&](int t) -> int {
+      const int key = k0 + t * kTK + (lane & 7) * 16;
+      if (t >= n_tiles || key >= k_end) return -1;
+      const int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + key / c.bt);
+      if (blk >= 0 && blk < c.n_blocks) return blk;
+      if (key + 16 > rg.lo) set_status(a.status, LC_DEV_BAD_BLOCK);
+      return -1;
+    };
+    auto fetch = [&](const uint8_t* base, int t, int pg, uint4 (&v)[kIt]) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int row = rsub + it * kRStep;
+        const int blk = __shfl_sync(0xffffffffu, pg, row >> 4);
+        v[it] = make_uint4(0, 0, 0, 0);
+        if (blk >= 0) {
+          const int key = k0 + t * kTK + row;
+          v[it] = __ldg(reinterpret_cast<const uint4*>(
+              base + ((static_cast<int64_t>(blk) * c.H_kv + h) * c.bt + key % c.bt) * D + piece * 16));
+        }
+      }
+    };
+    auto widen = [&](uint8_t* tile, const uint4 (&v)[kIt]) {
+      const int first = (piece >> 2) & 1;  // pieces of the second half store their odd chunk first: no bank conflicts
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int row = rsub + it * kRStep;
+        const uint4 lo = make_uint4(widen2(v[it].x), widen2(v[it].x >> 16), widen2(v[it].y), widen2(v[it].y >> 16));
+        const uint4 hi = make_uint4(widen2(v[it].z), widen2(v[it].z >> 16), widen2(v[it].w), widen2(v[it].w >> 16));
+        const int j = (piece & 3) * 2;
+        *reinterpret_cast<uint4*>(tile + tile_off(row, piece >> 2, j + first)) = first ? hi : lo;
+        *reinterpret_cast<uint4*>(tile + tile_off(row, piece >> 2, j + 1 - first)) = first ? lo : hi;
+      }
+    };
+    uint4 kr[kIt], vr[kIt];
+    int pg = page(0), pg_next = page(1);
+    fetch(c.k, 0, pg, kr);
+    fetch(c.v, 0, pg, vr);
+    for (int t = 0; t < n_tiles; ++t) {
+      const int st = t & 1;
+      uint8_t bk = 127, bv = 127;
+      if (cw == 0 && lane < 8 && pg >= 0) {
+        bk = __ldg(c.k_scale + static_cast<int64_t>(pg) * c.H_kv + h);
+        bv = __ldg(c.v_scale + static_cast<int64_t>(pg) * c.H_kv + h);
+      }
+      if (t >= 2) ok = wait(&bars.kempty[st], ((t >> 1) - 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (cw == 0 && lane < 8)
+        s_sc[t & 3][lane] = pg < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                   : make_float4(pow2f(kv8_exp(bk)), static_cast<float>(kv8_exp(bv)), pow2f(-kv8_exp(bv)), 0.f);
+      widen(Ks + st * kTile, kr);
+      fence_async_smem();
+      mbar_arrive(su32(&bars.kfull[st]));
+      fetch(c.k, t + 1, pg_next, kr);
+      if (t >= 2) ok = wait(&bars.vempty[st], ((t >> 1) - 1) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int t0 = k0 + t * kTK;
+      if (t0 < all_lo || t0 + kTK > all_hi) {
+        // rows that nobody sees may hold anything, and not every row of the CTA sees the others
+#pragma unroll
+        for (int it = 0; it < kIt; ++it) {
+          const int key = t0 + rsub + it * kRStep;
+          const bool out = key < rg.lo || key >= rg.hi;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&vr[it]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t m = out ? 0xffffffffu : nan_bytes(w[j]);
+            nan_seen |= !out && m != 0;
+            w[j] &= ~m;
+          }
+        }
+      }
+      widen(Vs + st * kTile, vr);
+      fence_async_smem();
+      mbar_arrive(su32(&bars.vfull[st]));
+      fetch(c.v, t + 1, pg_next, vr);
+      pg = pg_next;
+      pg_next = page(t + 2);
+    }
+    if (nan_seen) s_nan = 1;
+    named_bar(1, kThreads);
+  } else {
+    // ---------------- products of row tile i
+    regs_dec<32>();
+    if (i < n_act && lane == 0) {
+      const uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(kTK >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
+      const uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
+      const uint64_t qd = sw128_desc(su32(Qs + i * kTile));
+      const uint32_t ts = tm + i * kTK, to = tm + kColO + i * 128;
+      bool ok = n_tiles == 0 || wait(&bars.qfull[i], 0);
+      int issued = 0;  // products of P V issued
+      for (int t = 0; ok && t < n_tiles; ++t) {
+        const int st = t & 1;
+        // S_i's columns hold P_i until P_i V is complete
+        ok = wait(&bars.kfull[st], (t >> 1) & 1) && (t == 0 || wait(&bars.ofull[i], (t - 1) & 1));
+        if (!ok) break;
+        fence_after();
+        const uint64_t kd = sw128_desc(su32(Ks + st * kTile));  // the address field counts 16 bytes
+  #pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = ((k / 4) * kHalf + (k % 4) * 32) / 16;
+          mma_f16(ts, qd + at, kd + at, id_s, k > 0);
+        }
+        mma_commit(su32(&bars.sfull[i]));
+        mma_commit(su32(&bars.kempty[st]));
+        ok = wait(&bars.vfull[st], (t >> 1) & 1) && wait(&bars.pfull[i], t & 1);
+        if (!ok) break;
+        fence_after();
+        const uint64_t vd = sw128_mn_desc(su32(Vs + st * kTile), kHalf);
+  #pragma unroll
+        for (int k = 0; k < kTK / 16; ++k)
+          mma_f16_ts(to, ts + k * 8, vd + k * (2048 / 16), id_o, t > 0 || k > 0);
+        mma_commit(su32(&bars.vempty[st]));
+        mma_commit(su32(&bars.ofull[i]));
+        ++issued;
+      }
+      // a role that gave up: its products complete before tensor memory is released
+      if (!ok) {
+        mma_commit(su32(&bars.ofull[i]));
+        for (int x = issued > 0 ? issued - 1 : 0; x <= issued; ++x)
+          for (long it = 0; it < kSpin && !mbar_test(su32(&bars.ofull[i]), x & 1); ++it) {
+          }
+      }
+    }
+    __syncwarp();
+    named_bar(1, kThreads);
+  }
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tm, 512);
+}
+
+cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,
+                               cudaStream_t st) {
+  auto go = [&](auto kernel, size_t smem) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kThreads, smem, st>>>(a, geo, ws_o, ws_ml);
+    return cudaGetLastError();
+  };
+  return a.cache.D == 128 ? go(k_kv8_attn_tc<128>, smem_bytes<128>()) : go(k_kv8_attn_tc<64>, smem_bytes<64>());
+}
+
+}  // namespace lc

@@ -70,6 +70,18 @@ __device__ __forceinline__ uint32_t kv8_value_nans(const lc_kv8_cache& c, int s,
   return m;
 }
 
+// How a call's rows and keys are spread over CTAs.
+struct Kv8Geom {
+  int g;          // query heads per shared head
+  int row_tiles;  // row tiles per (sequence, shared head)
+  int n_split;    // CTAs per row tile (1: no split); of k_kv8_attn an upper bound
+  int rows;       // rows per row tile
+  int tc;         // k_kv8_attn_tc: every row has n_split partial results
+};
+
+cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,
+                               cudaStream_t st);
+
 // The output of one row from its joined partial result: the factor on O, and lse.
 __device__ __forceinline__ float kv8_finish(float R, float l, const float* sink, int head, float* lse) {
   if (!sink) {
