@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const lc_kv8_cache& c = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
+  const int bt_log = __ffs(c.bt) - 1;
   int64_t u = blockIdx.x;
   const int split = static_cast<int>(u % geo.n_split);
   u /= geo.n_split;
@@ -185,8 +186,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   bool nan_seen = false;  // NaN value codes replaced in an edge step
   for (int c0 = k_begin; c0 < k_end; c0 += kChunk) {
     const int c1 = min(k_end, c0 + kChunk);
-    const int pg0 = c0 / c.bt;
-    const int n_pg = (c1 - 1) / c.bt - pg0 + 1;
+    const int pg0 = c0 >> bt_log;
+    const int n_pg = ((c1 - 1) >> bt_log) - pg0 + 1;
     if (c0 > k_begin) __syncthreads();
     for (int i = tid; i < n_pg; i += kThreads) {
       int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + pg0 + i);
@@ -203,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 
     Step<D> cur, nxt;
     auto load = [&](int t0, Step<D>& st) {
-      const int pg = t0 < c1 ? s_page[t0 / c.bt - pg0] : -1;
+      const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
       if (pg < 0) return;  // never used
-      const int64_t at = ((static_cast<int64_t>(pg) * c.H_kv + h) * c.bt + t0 % c.bt) * D;
+      const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
       const uint8_t* kp = c.k + at + g8 * D + 16 * t4;
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     load(c0 + warp * 16, cur);
     for (int t0 = c0 + warp * 16; t0 < c1; t0 += 16 * kWarps) {
       load(t0 + 16 * kWarps, nxt);
-      const int ip = t0 / c.bt - pg0;
+      const int ip = (t0 >> bt_log) - pg0;
       if (s_page[ip] >= 0) {
         const float kf = s_kf[ip], ev = s_ev[ip];
         const float un_ev = pow2f(-static_cast<int>(ev));

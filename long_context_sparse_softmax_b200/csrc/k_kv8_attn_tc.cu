@@ -43,9 +43,11 @@ struct Bars {
   uint64_t ofull[2];   // O_i updated (commit)
 };
 
-__device__ __forceinline__ uint32_t widen2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// true in one lane of the (converged) warp; a branch on it leaves the other registers warp-uniform
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 // D += A B with A (128 rows x 16 F16 values) in tensor memory
@@ -70,12 +72,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// a shared-memory load that stays where it is written: hoisted, the scales of a tile's eight key
-// groups would hold 32 registers
-__device__ __forceinline__ float4 ld_shared4(const float4* p) {
+// shared-memory loads that stay where they are written: hoisted, a tile's scales would take registers
+__device__ __forceinline__ float4 ld_shared4(const void* p) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(su32(p)) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// pairs of FP32 values (one instruction for two products or sums)
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1,%2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, uint64_t m, uint64_t c) {
+  asm("{\n.reg .b64 t;\nmov.b64 t, {%0,%1};\nfma.rn.f32x2 t, t, %2, %3;\nmov.b64 {%0,%1}, t;\n}\n" : "+r"(x), "+r"(y) : "l"(m), "l"(c));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
 }
 
 template <int N>
@@ -113,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) Bars bars;
 
   const lc_kv8_cache& c = a.cache;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   int64_t u = blockIdx.x;
   const int split = static_cast<int>(u % geo.n_split);
   u /= geo.n_split;
@@ -153,6 +177,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicExch(&s_abort, 1);
     return false;
   };
+
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
   if (warp == 12) tmem_alloc(su32(&s_tmem), 512);
   if (tid == 0) {
@@ -236,48 +262,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         fence_after();
+        // y = x + ev - R and the weights 2^y, 32 keys at a time
         uint32_t pk[kTK / 2];
-        float ls = 0.f, al = 1.f;
-        bool first = true, again;
+        float ls, al = 1.f;
+        bool again = false;
         do {
+          const bool second = again;
           const float Ru = R == -INFINITY ? 0.f : R;
+          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the tile
+          asm volatile("" : "+r"(d_lo), "+r"(d_hi));
           float ymax = -INFINITY;
           ls = 0.f;
-          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the tile
-          asm volatile("" : "+r"(d_lo), "+r"(d_hi));  // keep their comparisons inside the loop
-          uint32_t sv[2][16];
-          tmem_ld16(ts, sv[0]);
+          uint32_t y[2][32];
+          tmem_ld32(ts, y[0]);
 #pragma unroll
-          for (int g = 0; g < kTK / 16; ++g) {
+          for (int x = 0; x < 4; ++x) {
             tmem_wait_ld();
-            if (g + 1 < kTK / 16) tmem_ld16(ts + (g + 1) * 16, sv[(g + 1) & 1]);
-            const float4 sc = ld_shared4(&s_sc[t & 3][g]);
-            const float fk = f_row * sc.x, off = sc.y - Ru;
-            float y[16];
+            if (x < 3) tmem_ld32(ts + (x + 1) * 32, y[(x + 1) & 1]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = fmaf(__uint_as_float(sv[g & 1][j]), fk, off);
-            if (edge) {
+            for (int g = 0; g < 2; ++g) {
+              const float4 sc = ld_shared4(&s_sc[t & 3][x * 2 + g]);
+              const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
+              uint32_t(&v)[32] = y[x & 1];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (g * 16 + j < d_lo || g * 16 + j >= d_hi) y[j] = -INFINITY;
+              for (int j = g * 16; j < g * 16 + 16; j += 2) fma2(v[j], v[j + 1], fk, off);
+              if (edge) {
+#pragma unroll
+                for (int j = g * 16; j < g * 16 + 16; ++j)
+                  if (x * 32 + j < d_lo || x * 32 + j >= d_hi) v[j] = 0xff800000u;
               }
-            }
-            float gs = 0.f;
+              uint64_t gs = 0;
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              ymax = fmaxf(ymax, fmaxf(y[j], y[j + 1]));
-              const float w0 = ex2(y[j]), w1 = ex2(y[j + 1]);
-              gs += w0 + w1;
-              const __half2 hv = __floats2half2_rn(w0, w1);
-              pk[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+              for (int j = g * 16; j < g * 16 + 16; j += 2) {
+                const float y0 = __uint_as_float(v[j]), y1 = __uint_as_float(v[j + 1]);
+                ymax = fmaxf(ymax, fmaxf(y0, y1));
+                const float w0 = ex2(y0), w1 = ex2(y1);
+                gs = add2(gs, pack2(w0, w1));
+                const __half2 hv = __floats2half2_rn(w0, w1);
+                pk[x * 16 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+              }
+              ls = fmaf(sum2(gs), sc.z, ls);
             }
-            ls = fmaf(gs, sc.z, ls);
           }
-          const bool need = first && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
+          const bool need = !second && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
           again = __any_sync(0xffffffffu, need);
-          first = false;
           if (need) {
-            // the reference moves: weigh the tile again
             al = ref_factor(R, Ru + ymax);
             R = Ru + ymax;
           }
@@ -299,13 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l = fmaf(l, al, ls);
-        uint32_t half[32];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) half[j] = pk[x * 32 + j];
-          tmem_st32(ts + x * 32, half);
-        }
+        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
         tmem_wait_st();
         fence_before();
         mbar_arrive(su32(&bars.pfull[i]));
@@ -376,11 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int all_lo = kv8_range(kv, a.W, pos(n_row - 1), pos(n_row - 1)).lo;  // keys that every row sees
     const int all_hi = kv8_range(kv, a.W, pos(0), pos(0)).hi;
     bool nan_seen = false, ok = true;
+    const int bt_log = __ffs(c.bt) - 1;
     // block of the tile's 16-key group lane % 8
     auto page = [&](int t) -> int {
       const int key = k0 + t * kTK + (lane & 7) * 16;
       if (t >= n_tiles || key >= k_end) return -1;
-      const int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + key / c.bt);
+      const int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + (key >> bt_log));
       if (blk >= 0 && blk < c.n_blocks) return blk;
       if (key + 16 > rg.lo) set_status(a.status, LC_DEV_BAD_BLOCK);
       return -1;
@@ -394,20 +419,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (blk >= 0) {
           const int key = k0 + t * kTK + row;
           v[it] = __ldg(reinterpret_cast<const uint4*>(
-              base + ((static_cast<int64_t>(blk) * c.H_kv + h) * c.bt + key % c.bt) * D + piece * 16));
+              base + (((static_cast<int64_t>(blk) * c.H_kv + h) << bt_log) + (key & (c.bt - 1))) * D + piece * 16));
         }
       }
     };
-    auto widen = [&](uint8_t* tile, const uint4 (&v)[kIt]) {
+    auto widen = [&](uint32_t tile, const uint4 (&v)[kIt]) {
       const int first = (piece >> 2) & 1;  // pieces of the second half store their odd chunk first: no bank conflicts
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
         const int row = rsub + it * kRStep;
-        const uint4 lo = make_uint4(widen2(v[it].x), widen2(v[it].x >> 16), widen2(v[it].y), widen2(v[it].y >> 16));
-        const uint4 hi = make_uint4(widen2(v[it].z), widen2(v[it].z >> 16), widen2(v[it].w), widen2(v[it].w >> 16));
+        const uint2 w0 = first ? make_uint2(v[it].z, v[it].w) : make_uint2(v[it].x, v[it].y);
+        const uint2 w1 = first ? make_uint2(v[it].x, v[it].y) : make_uint2(v[it].z, v[it].w);
+        uint32_t o[8];
+        widen4(w0.x, o[0], o[1]);
+        widen4(w0.y, o[2], o[3]);
+        widen4(w1.x, o[4], o[5]);
+        widen4(w1.y, o[6], o[7]);
         const int j = (piece & 3) * 2;
-        *reinterpret_cast<uint4*>(tile + tile_off(row, piece >> 2, j + first)) = first ? hi : lo;
-        *reinterpret_cast<uint4*>(tile + tile_off(row, piece >> 2, j + 1 - first)) = first ? lo : hi;
+        st_shared4(tile + tile_off(row, piece >> 2, j + first), o[0], o[1], o[2], o[3]);
+        st_shared4(tile + tile_off(row, piece >> 2, j + 1 - first), o[4], o[5], o[6], o[7]);
       }
     };
     uint4 kr[kIt], vr[kIt];
@@ -426,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cw == 0 && lane < 8)
         s_sc[t & 3][lane] = pg < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
                                    : make_float4(pow2f(kv8_exp(bk)), static_cast<float>(kv8_exp(bv)), pow2f(-kv8_exp(bv)), 0.f);
-      widen(Ks + st * kTile, kr);
+      widen(su32(Ks + st * kTile), kr);
       fence_async_smem();
       mbar_arrive(su32(&bars.kfull[st]));
       fetch(c.k, t + 1, pg_next, kr);
@@ -448,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      widen(Vs + st * kTile, vr);
+      widen(su32(Vs + st * kTile), vr);
       fence_async_smem();
       mbar_arrive(su32(&bars.vfull[st]));
       fetch(c.v, t + 1, pg_next, vr);
@@ -460,40 +490,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- products of row tile i
     regs_dec<32>();
-    if (i < n_act && lane == 0) {
+    if (i < n_act) {
+      const bool one = elect_one();
       const uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(kTK >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
       const uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
       const uint64_t qd = sw128_desc(su32(Qs + i * kTile));
       const uint32_t ts = tm + i * kTK, to = tm + kColO + i * 128;
-      bool ok = n_tiles == 0 || wait(&bars.qfull[i], 0);
+      bool ok = n_tiles == 0 || wait_all(&bars.qfull[i], 0);
       int issued = 0;  // products of P V issued
       for (int t = 0; ok && t < n_tiles; ++t) {
         const int st = t & 1;
         // S_i's columns hold P_i until P_i V is complete
-        ok = wait(&bars.kfull[st], (t >> 1) & 1) && (t == 0 || wait(&bars.ofull[i], (t - 1) & 1));
+        ok = wait_all(&bars.kfull[st], (t >> 1) & 1) && (t == 0 || wait_all(&bars.ofull[i], (t - 1) & 1));
         if (!ok) break;
         fence_after();
         const uint64_t kd = sw128_desc(su32(Ks + st * kTile));  // the address field counts 16 bytes
-  #pragma unroll
+          if (one) {
+#pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t at = ((k / 4) * kHalf + (k % 4) * 32) / 16;
           mma_f16(ts, qd + at, kd + at, id_s, k > 0);
         }
         mma_commit(su32(&bars.sfull[i]));
         mma_commit(su32(&bars.kempty[st]));
-        ok = wait(&bars.vfull[st], (t >> 1) & 1) && wait(&bars.pfull[i], t & 1);
+        }
+        ok = wait_all(&bars.vfull[st], (t >> 1) & 1) && wait_all(&bars.pfull[i], t & 1);
         if (!ok) break;
         fence_after();
         const uint64_t vd = sw128_mn_desc(su32(Vs + st * kTile), kHalf);
-  #pragma unroll
+          if (one) {
+#pragma unroll
         for (int k = 0; k < kTK / 16; ++k)
           mma_f16_ts(to, ts + k * 8, vd + k * (2048 / 16), id_o, t > 0 || k > 0);
         mma_commit(su32(&bars.vempty[st]));
         mma_commit(su32(&bars.ofull[i]));
+        }
         ++issued;
       }
       // a role that gave up: its products complete before tensor memory is released
-      if (!ok) {
+      if (!ok && one) {
         mma_commit(su32(&bars.ofull[i]));
         for (int x = issued > 0 ? issued - 1 : 0; x <= issued; ++x)
           for (long it = 0; it < kSpin && !mbar_test(su32(&bars.ofull[i]), x & 1); ++it) {

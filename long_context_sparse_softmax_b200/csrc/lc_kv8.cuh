@@ -70,6 +70,13 @@ __device__ __forceinline__ uint32_t kv8_value_nans(const lc_kv8_cache& c, int s,
   return m;
 }
 
+// four E4M3 codes -> two pairs of F16 values (exact)
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& a, uint32_t& b) {
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(v));
+}
+
 // How a call's rows and keys are spread over CTAs.
 struct Kv8Geom {
   int g;          // query heads per shared head
