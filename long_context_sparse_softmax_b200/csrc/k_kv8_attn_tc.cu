@@ -27,20 +27,22 @@ namespace lc {
 namespace {
 
 constexpr int kTK = 128;                 // keys per tile
+constexpr int kHK = 64;                  // keys per product with Q and per softmax step
 constexpr int kRT = 128;                 // rows per row tile
 constexpr int kThreads = 512;
 constexpr float kHeadroom = 8.f;
-constexpr long kSpin = 1L << 26;
-constexpr uint32_t kColO = 256;          // S_i at 128 i, O_i at 256 + 128 i
+constexpr long kSpin = 1L << 20;         // a few seconds
+constexpr uint32_t kColO = 256;          // S_i at 128 i (two half tiles), O_i at 256 + 128 i
 constexpr int kHalf = kTK * 128;         // bytes of 128 rows x 64 F16 values (SWIZZLE_128B)
 
 struct Bars {
   uint64_t qfull[2];   // Q_i in shared memory (128 arrivals)
+  uint64_t fin[2];     // a role that gave up: its products are complete (commit)
   uint64_t kfull[2], vfull[2];    // stage written (128)
   uint64_t kempty[2], vempty[2];  // stage read by every row tile (commits)
-  uint64_t sfull[2];   // S_i computed (commit)
-  uint64_t pfull[2];   // P_i written, O_i rescaled (128)
-  uint64_t ofull[2];   // O_i updated (commit)
+  uint64_t sfull[2][2];  // S_i of a half tile computed (commit), its scales in shared memory (the issuer's arrival)
+  uint64_t pfull[2][2];  // P_i written, O_i rescaled (128)
+  uint64_t ofull[2][2];  // O_i updated (commit)
 };
 
 // true in one lane of the (converged) warp; a branch on it leaves the other registers warp-uniform
@@ -185,13 +187,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_abort = s_nan = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(su32(&bars.qfull[i]), 128);
+      mbar_init(su32(&bars.fin[i]), 1);
       mbar_init(su32(&bars.kfull[i]), 128);
       mbar_init(su32(&bars.vfull[i]), 128);
       mbar_init(su32(&bars.kempty[i]), n_act);
       mbar_init(su32(&bars.vempty[i]), n_act);
-      mbar_init(su32(&bars.sfull[i]), 1);
-      mbar_init(su32(&bars.pfull[i]), 128);
-      mbar_init(su32(&bars.ofull[i]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(su32(&bars.sfull[i][b]), 2);
+        mbar_init(su32(&bars.pfull[i][b]), 128);
+        mbar_init(su32(&bars.ofull[i][b]), 1);
+      }
     }
     fence_mbar_init();
   }
@@ -253,56 +258,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_lo = kv8_range(kv, a.W, pos(last_r), pos(last_r)).lo;
       const uint32_t ts = tm + lane_off + i * kTK, to = tm + lane_off + kColO + i * 128;
 
-      for (int t = 0; t < n_tiles; ++t) {
-        const int t0 = k0 + t * kTK;
-        const bool edge = t0 < all_lo || t0 + kTK > all_hi;
-        const bool ok = wait(&bars.sfull[i], t & 1) && wait(&bars.kfull[t & 1], (t >> 1) & 1);
+      for (int hh = 0; hh < 2 * n_tiles; ++hh) {
+        const int t = hh >> 1, bf = hh & 1;
+        const int t0 = k0 + hh * kHK;
+        const bool edge = t0 < all_lo || t0 + kHK > all_hi;
+        const bool ok = wait(&bars.sfull[i][bf], t & 1);
         if (!__all_sync(0xffffffffu, ok)) {
           good = false;
           break;
         }
         fence_after();
-        // y = x + ev - R and the weights 2^y, 32 keys at a time
-        uint32_t pk[kTK / 2];
+        // y = x + ev - R and the weights 2^y
+        uint32_t pk[kHK / 2];
         float ls, al = 1.f;
         bool again = false;
         do {
           const bool second = again;
           const float Ru = R == -INFINITY ? 0.f : R;
-          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the tile
+          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the half tile
           asm volatile("" : "+r"(d_lo), "+r"(d_hi));
           float ymax = -INFINITY;
           ls = 0.f;
           uint32_t y[2][32];
-          tmem_ld32(ts, y[0]);
+          tmem_ld32(ts + bf * kHK, y[0]);
+          tmem_ld32(ts + bf * kHK + 32, y[1]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            tmem_wait_ld();
-            if (x < 3) tmem_ld32(ts + (x + 1) * 32, y[(x + 1) & 1]);
+          for (int g = 0; g < kHK / 16; ++g) {
+            const float4 sc = ld_shared4(&s_sc[t & 3][bf * 4 + g]);
+            const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
+            uint32_t* v = y[g / 2] + (g & 1) * 16;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float4 sc = ld_shared4(&s_sc[t & 3][x * 2 + g]);
-              const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
-              uint32_t(&v)[32] = y[x & 1];
+            for (int j = 0; j < 16; j += 2) fma2(v[j], v[j + 1], fk, off);
+            if (edge) {
 #pragma unroll
-              for (int j = g * 16; j < g * 16 + 16; j += 2) fma2(v[j], v[j + 1], fk, off);
-              if (edge) {
-#pragma unroll
-                for (int j = g * 16; j < g * 16 + 16; ++j)
-                  if (x * 32 + j < d_lo || x * 32 + j >= d_hi) v[j] = 0xff800000u;
-              }
-              uint64_t gs = 0;
-#pragma unroll
-              for (int j = g * 16; j < g * 16 + 16; j += 2) {
-                const float y0 = __uint_as_float(v[j]), y1 = __uint_as_float(v[j + 1]);
-                ymax = fmaxf(ymax, fmaxf(y0, y1));
-                const float w0 = ex2(y0), w1 = ex2(y1);
-                gs = add2(gs, pack2(w0, w1));
-                const __half2 hv = __floats2half2_rn(w0, w1);
-                pk[x * 16 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
-              }
-              ls = fmaf(sum2(gs), sc.z, ls);
+              for (int j = 0; j < 16; ++j)
+                if (g * 16 + j < d_lo || g * 16 + j >= d_hi) v[j] = 0xff800000u;
             }
+            uint64_t gs = 0;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float y0 = __uint_as_float(v[j]), y1 = __uint_as_float(v[j + 1]);
+              ymax = fmaxf(ymax, fmaxf(y0, y1));
+              const float w0 = ex2(y0), w1 = ex2(y1);
+              gs = add2(gs, pack2(w0, w1));
+              const __half2 hv = __floats2half2_rn(w0, w1);
+              pk[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+            ls = fmaf(sum2(gs), sc.z, ls);
           }
           const bool need = !second && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
           again = __any_sync(0xffffffffu, need);
@@ -311,8 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             R = Ru + ymax;
           }
         } while (again);
-        if (__any_sync(0xffffffffu, al != 1.f) && t > 0) {
-          if (!__all_sync(0xffffffffu, wait(&bars.ofull[i], (t - 1) & 1))) {
+        if (__any_sync(0xffffffffu, al != 1.f) && hh > 0) {
+          if (!__all_sync(0xffffffffu, wait(&bars.ofull[i][bf ^ 1], ((hh - 1) >> 1) & 1))) {
             good = false;
             break;
           }
@@ -328,13 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         l = fmaf(l, al, ls);
-        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
-        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+        tmem_st32(ts + bf * kHK, pk);
         tmem_wait_st();
         fence_before();
-        mbar_arrive(su32(&bars.pfull[i]));
+        mbar_arrive(su32(&bars.pfull[i][bf]));
       }
-      if (good && n_tiles > 0) good = __all_sync(0xffffffffu, wait(&bars.ofull[i], (n_tiles - 1) & 1));
+      if (good && n_tiles > 0) good = __all_sync(0xffffffffu, wait(&bars.ofull[i][1], (n_tiles - 1) & 1));
     }
     named_bar(1, kThreads);
     // ---------------- output: a thread per row
@@ -492,47 +494,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<32>();
     if (i < n_act) {
       const bool one = elect_one();
-      const uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(kTK >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
+      const uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(kHK >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
       const uint32_t id_o = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
-      const uint64_t qd = sw128_desc(su32(Qs + i * kTile));
+      const uint64_t qd = sw128_desc(su32(Qs + i * kTile));  // the address field counts 16 bytes
       const uint32_t ts = tm + i * kTK, to = tm + kColO + i * 128;
-      bool ok = n_tiles == 0 || wait_all(&bars.qfull[i], 0);
-      int issued = 0;  // products of P V issued
-      for (int t = 0; ok && t < n_tiles; ++t) {
-        const int st = t & 1;
-        // S_i's columns hold P_i until P_i V is complete
-        ok = wait_all(&bars.kfull[st], (t >> 1) & 1) && (t == 0 || wait_all(&bars.ofull[i], (t - 1) & 1));
+      const int n_half = 2 * n_tiles;
+      // S of half tile hh; its columns hold P of hh - 2 until that is used up
+      auto issue_s = [&](int hh) -> bool {
+        const int t = hh >> 1, st = t & 1, bf = hh & 1;
+        if (!wait_all(&bars.kfull[st], (t >> 1) & 1) || (hh >= 2 && !wait_all(&bars.ofull[i][bf], (t - 1) & 1))) return false;
+        fence_after();
+        const uint64_t kd = sw128_desc(su32(Ks + st * kTile)) + bf * (kHK * 128 / 16);
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = ((k / 4) * kHalf + (k % 4) * 32) / 16;
+            mma_f16(ts + bf * kHK, qd + at, kd + at, id_s, k > 0);
+          }
+          mma_commit(su32(&bars.sfull[i][bf]));
+          mbar_arrive(su32(&bars.sfull[i][bf]));
+          if (bf) mma_commit(su32(&bars.kempty[st]));
+        }
+        return true;
+      };
+      bool ok = n_tiles == 0 || (wait_all(&bars.qfull[i], 0) && issue_s(0) && issue_s(1));
+      for (int hh = 0; ok && hh < n_half; ++hh) {
+        const int t = hh >> 1, st = t & 1, bf = hh & 1;
+        ok = wait_all(&bars.vfull[st], (t >> 1) & 1) && wait_all(&bars.pfull[i][bf], t & 1);
         if (!ok) break;
         fence_after();
-        const uint64_t kd = sw128_desc(su32(Ks + st * kTile));  // the address field counts 16 bytes
-          if (one) {
+        const uint64_t vd = sw128_mn_desc(su32(Vs + st * kTile), kHalf) + bf * (kHK * 128 / 16);
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = ((k / 4) * kHalf + (k % 4) * 32) / 16;
-          mma_f16(ts, qd + at, kd + at, id_s, k > 0);
+          for (int k = 0; k < kHK / 16; ++k)
+            mma_f16_ts(to, ts + bf * kHK + k * 8, vd + k * (2048 / 16), id_o, hh > 0 || k > 0);
+          mma_commit(su32(&bars.ofull[i][bf]));
+          if (bf) mma_commit(su32(&bars.vempty[st]));
         }
-        mma_commit(su32(&bars.sfull[i]));
-        mma_commit(su32(&bars.kempty[st]));
-        }
-        ok = wait_all(&bars.vfull[st], (t >> 1) & 1) && wait_all(&bars.pfull[i], t & 1);
-        if (!ok) break;
-        fence_after();
-        const uint64_t vd = sw128_mn_desc(su32(Vs + st * kTile), kHalf);
-          if (one) {
-#pragma unroll
-        for (int k = 0; k < kTK / 16; ++k)
-          mma_f16_ts(to, ts + k * 8, vd + k * (2048 / 16), id_o, t > 0 || k > 0);
-        mma_commit(su32(&bars.vempty[st]));
-        mma_commit(su32(&bars.ofull[i]));
-        }
-        ++issued;
+        if (hh + 2 < n_half) ok = issue_s(hh + 2);
       }
       // a role that gave up: its products complete before tensor memory is released
       if (!ok && one) {
-        mma_commit(su32(&bars.ofull[i]));
-        for (int x = issued > 0 ? issued - 1 : 0; x <= issued; ++x)
-          for (long it = 0; it < kSpin && !mbar_test(su32(&bars.ofull[i]), x & 1); ++it) {
-          }
+        mma_commit(su32(&bars.fin[i]));
+        for (long it = 0; it < kSpin && !mbar_test(su32(&bars.fin[i]), 0); ++it) {
+        }
       }
     }
     __syncwarp();

@@ -32,7 +32,7 @@ constexpr int kK = 128;                 // inputs per step
 constexpr int kTileA = kM * kK;         // bytes of A in shared memory (padded codes)
 constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 rows of 4 words
 constexpr int kThreads = 288;
-constexpr long kSpin = 1L << 26;
+constexpr long kSpin = 1L << 20;  // a few seconds
 constexpr int kMaxTok = 64;             // rows of x per CTA
 
 // stages of the ring for N columns of B
