@@ -75,9 +75,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 // shared-memory loads that stay where they are written: hoisted, a tile's scales would take registers
-__device__ __forceinline__ float4 ld_shared4(const void* p) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(su32(p)) : "memory");
+__device__ __forceinline__ float2 ld_shared2(const void* p) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(su32(p)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_shared1(const void* p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(su32(p)) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -285,16 +290,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < kHK / 16; ++g) {
-            const float4 sc = ld_shared4(&s_sc[t & 3][bf * 4 + g]);
+            const float2 sc = ld_shared2(&s_sc[t & 3][bf * 4 + g]);
             const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
             uint32_t* v = y[g / 2] + (g & 1) * 16;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) fma2(v[j], v[j + 1], fk, off);
-            if (edge) {
+          }
+          if (edge) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (g * 16 + j < d_lo || g * 16 + j >= d_hi) v[j] = 0xff800000u;
-            }
+            for (int j = 0; j < kHK; ++j)
+              if (j < d_lo || j >= d_hi) y[j / 32][j % 32] = 0xff800000u;
+          }
+#pragma unroll
+          for (int g = 0; g < kHK / 16; ++g) {
+            const uint32_t* v = y[g / 2] + (g & 1) * 16;
             uint64_t gs = 0;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -305,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __half2 hv = __floats2half2_rn(w0, w1);
               pk[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
             }
-            ls = fmaf(sum2(gs), sc.z, ls);
+            ls = fmaf(sum2(gs), ld_shared1(&s_sc[t & 3][bf * 4 + g].z), ls);
           }
           const bool need = !second && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
           again = __any_sync(0xffffffffu, need);
@@ -396,72 +405,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 12) {
     // ---------------- codes -> F16 tiles
     regs_dec<96>();
-    const int ct = tid - 256, cw = warp - 8;
-    const int piece = ct % kPR, rsub = ct / kPR;  // rows rsub + it * (128 / kPR)
-    constexpr int kRStep = 128 / kPR;             // 16 (D = 128) or 32 (D = 64)
+    const int cw = warp - 8;
+    // a warp's 32 pieces are whole rows (512 bytes); the eight lanes of a 16-byte store phase take four
+    // pieces of two neighbouring rows, whose chunks fall into different banks
+    const int piece = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+    const int rsub = D == 128 ? cw * 4 + (lane >> 2 & 1) + (lane >> 4) * 2 : cw * 8 + (lane >> 2);
+    constexpr int kRStep = 128 / kPR;             // rows rsub + it * kRStep
     const int all_lo = kv8_range(kv, a.W, pos(n_row - 1), pos(n_row - 1)).lo;  // keys that every row sees
     const int all_hi = kv8_range(kv, a.W, pos(0), pos(0)).hi;
     bool nan_seen = false, ok = true;
     const int bt_log = __ffs(c.bt) - 1;
-    // block of the tile's 16-key group lane % 8
-    auto page = [&](int t) -> int {
+    const int64_t slot_bytes = static_cast<int64_t>(D) << bt_log;
+    // block * H_kv + h of the tile's 16-key group lane % 8, -1: none
+    auto slot = [&](int t) -> int {
       const int key = k0 + t * kTK + (lane & 7) * 16;
       if (t >= n_tiles || key >= k_end) return -1;
       const int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + (key >> bt_log));
-      if (blk >= 0 && blk < c.n_blocks) return blk;
+      if (blk >= 0 && blk < c.n_blocks) return blk * c.H_kv + h;
       if (key + 16 > rg.lo) set_status(a.status, LC_DEV_BAD_BLOCK);
       return -1;
     };
-    auto fetch = [&](const uint8_t* base, int t, int pg, uint4 (&v)[kIt]) {
+    // tiles start at multiples of 128, of every block size: a row's place in its block is the same in each
+    auto fetch = [&](const uint8_t* base, int sl, uint4 (&v)[kIt]) {
+      const bool whole = __all_sync(0xffffffffu, sl >= 0);
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
         const int row = rsub + it * kRStep;
-        const int blk = __shfl_sync(0xffffffffu, pg, row >> 4);
-        v[it] = make_uint4(0, 0, 0, 0);
-        if (blk >= 0) {
-          const int key = k0 + t * kTK + row;
-          v[it] = __ldg(reinterpret_cast<const uint4*>(
-              base + (((static_cast<int64_t>(blk) * c.H_kv + h) << bt_log) + (key & (c.bt - 1))) * D + piece * 16));
-        }
+        const int sr = __shfl_sync(0xffffffffu, sl, row >> 4);
+        const uint8_t* p = base + sr * slot_bytes + (row & (c.bt - 1)) * D + piece * 16;
+        if (!whole) v[it] = make_uint4(0, 0, 0, 0);
+        if (whole || sr >= 0) v[it] = __ldg(reinterpret_cast<const uint4*>(p));
       }
     };
     auto widen = [&](uint32_t tile, const uint4 (&v)[kIt]) {
-      const int first = (piece >> 2) & 1;  // pieces of the second half store their odd chunk first: no bank conflicts
+      const uint32_t lo = tile + tile_off(rsub, piece >> 2, (piece & 3) * 2), hi = tile + tile_off(rsub, piece >> 2, (piece & 3) * 2 + 1);
 #pragma unroll
       for (int it = 0; it < kIt; ++it) {
-        const int row = rsub + it * kRStep;
-        const uint2 w0 = first ? make_uint2(v[it].z, v[it].w) : make_uint2(v[it].x, v[it].y);
-        const uint2 w1 = first ? make_uint2(v[it].x, v[it].y) : make_uint2(v[it].z, v[it].w);
         uint32_t o[8];
-        widen4(w0.x, o[0], o[1]);
-        widen4(w0.y, o[2], o[3]);
-        widen4(w1.x, o[4], o[5]);
-        widen4(w1.y, o[6], o[7]);
-        const int j = (piece & 3) * 2;
-        st_shared4(tile + tile_off(row, piece >> 2, j + first), o[0], o[1], o[2], o[3]);
-        st_shared4(tile + tile_off(row, piece >> 2, j + 1 - first), o[4], o[5], o[6], o[7]);
+        widen4(v[it].x, o[0], o[1]);
+        widen4(v[it].y, o[2], o[3]);
+        widen4(v[it].z, o[4], o[5]);
+        widen4(v[it].w, o[6], o[7]);
+        // rows 16 (or 32) apart have the same place in the swizzle
+        st_shared4(lo + it * kRStep * 128, o[0], o[1], o[2], o[3]);
+        st_shared4(hi + it * kRStep * 128, o[4], o[5], o[6], o[7]);
       }
     };
     uint4 kr[kIt], vr[kIt];
-    int pg = page(0), pg_next = page(1);
-    fetch(c.k, 0, pg, kr);
-    fetch(c.v, 0, pg, vr);
+    int sl = slot(0), sl_next = slot(1);
+    fetch(c.k, sl, kr);
+    fetch(c.v, sl, vr);
     for (int t = 0; t < n_tiles; ++t) {
       const int st = t & 1;
       uint8_t bk = 127, bv = 127;
-      if (cw == 0 && lane < 8 && pg >= 0) {
-        bk = __ldg(c.k_scale + static_cast<int64_t>(pg) * c.H_kv + h);
-        bv = __ldg(c.v_scale + static_cast<int64_t>(pg) * c.H_kv + h);
+      if (cw == 0 && lane < 8 && sl >= 0) {
+        bk = __ldg(c.k_scale + sl);
+        bv = __ldg(c.v_scale + sl);
       }
       if (t >= 2) ok = wait(&bars.kempty[st], ((t >> 1) - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       if (cw == 0 && lane < 8)
-        s_sc[t & 3][lane] = pg < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+        s_sc[t & 3][lane] = sl < 0 ? make_float4(0.f, -INFINITY, 0.f, 0.f)
                                    : make_float4(pow2f(kv8_exp(bk)), static_cast<float>(kv8_exp(bv)), pow2f(-kv8_exp(bv)), 0.f);
       widen(su32(Ks + st * kTile), kr);
       fence_async_smem();
       mbar_arrive(su32(&bars.kfull[st]));
-      fetch(c.k, t + 1, pg_next, kr);
+      fetch(c.k, sl_next, kr);
       if (t >= 2) ok = wait(&bars.vempty[st], ((t >> 1) - 1) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       const int t0 = k0 + t * kTK;
@@ -483,9 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       widen(su32(Vs + st * kTile), vr);
       fence_async_smem();
       mbar_arrive(su32(&bars.vfull[st]));
-      fetch(c.v, t + 1, pg_next, vr);
-      pg = pg_next;
-      pg_next = page(t + 2);
+      fetch(c.v, sl_next, vr);
+      sl = sl_next;
+      sl_next = slot(t + 2);
     }
     if (nan_seen) s_nan = 1;
     named_bar(1, kThreads);

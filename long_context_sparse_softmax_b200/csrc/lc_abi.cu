@@ -196,6 +196,7 @@ lc_status check_kv8(const lc_kv8_cache& c, bool need) {
   if ((c.D != 64 && c.D != 128) || (c.bt != 16 && c.bt != 32 && c.bt != 64 && c.bt != 128)) return LC_ERR_UNSUPPORTED;
   // token positions are 32-bit
   if (static_cast<int64_t>(c.table_cols) * c.bt > INT32_MAX) return LC_ERR_ARG;
+  if (static_cast<int64_t>(c.n_blocks) * c.H_kv > INT32_MAX) return LC_ERR_ARG;  // so are block slots
   if (!need) return LC_OK;
   if (!c.k || !c.v || !c.k_scale || !c.v_scale || !c.table) return LC_ERR_ARG;
   if (!aligned16(c.k) || !aligned16(c.v)) return LC_ERR_ALIGN;
