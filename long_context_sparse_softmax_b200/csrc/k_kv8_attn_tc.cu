@@ -45,13 +45,6 @@ struct Bars {
   uint64_t ofull[2][2];  // O_i updated (commit)
 };
 
-// true in one lane of the (converged) warp; a branch on it leaves the other registers warp-uniform
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
-}
-
 // D += A B with A (128 rows x 16 F16 values) in tensor memory
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(

@@ -10,15 +10,17 @@
 // fits the other 4: hi + lo is x exactly down to 2^-15 of the block's largest value.
 //
 // A CTA holds one tile of 128 outputs of a group and a range of its inputs, in steps of 128:
-//   * warps 0-3 copy the codes (cp.async, 8 bytes = 16 codes into each 16-byte slot of the
+//   * warps 0-7 copy the codes (cp.async, 8 bytes = 16 codes into each 16-byte slot of the
 //     SWIZZLE_128B layout: the tensor core reads 4-bit operands with 8 bytes of padding behind
 //     every 16 values) and the scale words, kAhead steps ahead, and run the epilogue;
-//   * warps 4-7 turn x into B's columns and scales;
-//   * lane 0 of warp 8 copies a step's scales into tensor memory and issues its four K = 32 MMAs.
+//   * warps 8-15 turn x into B's columns and scales;
+//   * one lane of warp 16 copies a step's scales into tensor memory and issues its four K = 32 MMAs.
 // A cluster of `split` CTAs shares a tile's inputs when there are fewer tiles than
 // multiprocessors; the partial tiles meet in distributed shared memory and are added in rank
 // order, so the result does not depend on timing.  Every mbarrier wait is bounded
 // (LC_DEV_TIMEOUT).
+#include <algorithm>
+
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
 #include "lc_ptx.cuh"
@@ -31,23 +33,63 @@ constexpr int kM = 128;                 // outputs per tile
 constexpr int kK = 128;                 // inputs per step
 constexpr int kTileA = kM * kK;         // bytes of A in shared memory (padded codes)
 constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 rows of 4 words
-constexpr int kThreads = 288;
+constexpr int kGroups = 2;               // groups of 4 warps that take steps in turn: for the weights, and for x
+constexpr int kMmaWarp = 8 * kGroups;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr long kSpin = 1L << 20;  // a few seconds
 constexpr int kMaxTok = 64;             // rows of x per CTA
 
-// stages of the ring for N columns of B
-template <int N>
-struct W4Ring {
-  static constexpr int kBytes = kTileA + N * kK + 2 * kSf;  // of a stage
-  static constexpr int kFit = 212 * 1024 / kBytes;
-  static constexpr int kStages = kFit < 10 ? kFit : 10;
+// shared memory for N columns of B: kRawW steps of codes and scale words as they come from memory,
+// kRawX steps of x, and kStages steps in the tensor core's layout
+template <int N, bool kMx>
+struct W4Smem {
+  static constexpr int kTok = kMx ? N : N / 2;
+  static constexpr int kU = kMx ? kTok / 16 : kTok / 8;   // 16-byte units of x per thread of a group and step
+  static constexpr int kStages = N <= 16 ? 6 : N <= 32 ? 5 : N <= 64 ? 4 : 3;
+  static constexpr int kRawX = N <= 64 ? 6 : 4;           // multiples of kGroups
+  static constexpr int kRawW = N <= 64 ? 8 : 6;
+  static constexpr int kStage = kTileA + N * kK + 2 * kSf;
+  static constexpr int kRawWBytes = kM * kK / 2 + kM * 4;
+  static constexpr int kRawXBytes = 128 * kU * 16 + (kMx ? kTok * 4 : 0);
+  static constexpr int kRing = kStages * kStage, kW = kRawW * kRawWBytes, kX = kRawX * kRawXBytes;
+  // a CTA's share of the joined rows is (n_tok + split - 1) / split rows of `split` partial sums; it lies
+  // where the codes were
+  static constexpr int kPart = (kTok + 7) * kM * 4;
+  static constexpr int kBytes = kRing + (kW > kPart ? kW : kPart) + kX + 1024;
 };
 
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_shared8(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ void st_shared1(uint32_t a, uint32_t x) {
+  asm volatile("st.shared.b8 [%0], %1;\n" ::"r"(a), "r"(x) : "memory");
 }
 
 // scale block (32 rows x 16 bytes) -> 4 columns of tensor memory, every lane quadrant
@@ -62,25 +104,26 @@ __device__ __forceinline__ void tmem_scales(uint32_t taddr, const void* smem) {
 // byte of row r, 32-value block b of a scale block
 __device__ __forceinline__ int sf_off(int r, int b) { return (r & 31) * 16 + (r >> 5) * 4 + b; }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(__half2 v) {
+  return __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint16_t v) { return __half2(__nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3)); }
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v) {
   uint32_t r;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(r) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(r), "f"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
 
 }  // namespace
 
 // N: columns of B (a multiple of 16: 2 per BF16 row, 1 per MXFP8 row)
 template <int N, bool kMx>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int split, int tiles_g) {
-  constexpr int kStages = W4Ring<N>::kStages;
-  constexpr int kAhead = kStages - 1;
-  constexpr int kTok = kMx ? N : N / 2;
+  using L = W4Smem<N, kMx>;
+  constexpr int kStages = L::kStages, kTok = L::kTok;
   constexpr uint32_t kCols = N + 16 <= 32 ? 32 : N + 16 <= 64 ? 64 : N + 16 <= 128 ? 128 : 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -88,12 +131,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   uint8_t* Bs = As + kStages * kTileA;             // [kStages][N * kK]
   uint8_t* SFa = Bs + kStages * N * kK;            // [kStages][kSf]
   uint8_t* SFb = SFa + kStages * kSf;              // [kStages][kSf]
-  float* part = reinterpret_cast<float*>(smem);    // after the last MMA: [kTok][kM]
+  uint8_t* Xr = SFb + kStages * kSf;               // [kRawX][kRawXBytes]
+  uint8_t* Wr = Xr + L::kX;                        // [kRawW][kRawWBytes]
+  // partial tiles of a cluster: the row's place in the share of the CTA that adds it up, rank, output
+  float* part = reinterpret_cast<float*>(Wr);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % split;
   const int tile = static_cast<int>(blockIdx.x) / split;
   const int g = tile / tiles_g;
@@ -116,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
     return false;
   };
 
-  if (warp == 8) tmem_alloc(su32(&s_tmem), kCols);
+  if (warp == kMmaWarp) tmem_alloc(su32(&s_tmem), kCols);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kStages; ++i) {
@@ -135,156 +181,198 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   fence_after();
   const uint32_t tm = s_tmem;
 
-  if (warp < 4) {
-    // ---------------- the weights
+  if (warp < 4 * kGroups) {
+    // ---------------- the weights: 16 bytes (32 codes) of 4 rows a thread and step, copied kRawW - 1
+    // steps ahead into places of the thread's own, then spread.  (Copies of 8 bytes would land in place by
+    // themselves, but took 950 cycles a step.)
     const int64_t row_g = static_cast<int64_t>(g) * a.d_g + c0;
-    const int piece = lane & 7;
+    const int grp = warp >> 2, gt = tid & 127;
+    const int seg = lane & 3, r0 = (warp & 3) * 8 + (lane >> 2);  // rows r0 + 32 j
     const bool words = a.K % 128 == 0;  // a row's four scale bytes of a step are one aligned word
-    bool ok = true;
-    for (int i = 0; ok && i < n_step + kAhead; ++i) {
+    const uint8_t* wp = a.w + (row_g + r0) * (a.K / 2) + static_cast<int64_t>(s_begin) * (kK / 2) + seg * 16;
+    const int64_t r32 = static_cast<int64_t>(a.K) * 16;      // 32 rows further
+    const uint8_t* sp = a.w_scale + (row_g + gt) * (a.K / 32) + s_begin * 4;
+    const uint32_t raw = su32(Wr) + gt * 16, raws = su32(Wr) + kM * kK / 2 + gt * 4;
+    auto copy = [&](int i, int slot) {
       if (i < n_step) {
-        const int st = i % kStages;
-        if (i >= kStages) ok = wait(&empty[st], ((i / kStages) - 1) & 1);
-        if (!ok) break;
-        const int k = (s_begin + i) * kK + piece * 16;
+        const uint8_t* p = wp + static_cast<int64_t>(i) * (kK / 2);
+        const bool k_in = (s_begin + i) * kK + seg * 32 < a.K;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = j * 16 + warp * 4 + (lane >> 3);
-          const bool v = r < rows && k < a.K;
-          const uint8_t* src = a.w + (v ? (row_g + r) * (a.K / 2) + k / 2 : 0);
-          cp_async8(su32(As + st * kTileA) + sw128_off(r, piece), src, v);
+        for (int j = 0; j < 4; ++j) {
+          const bool v = k_in && r0 + 32 * j < rows;
+          cp_async16z(raw + slot * L::kRawWBytes + j * 2048, v ? p + j * r32 : a.w, v);
         }
-        uint8_t* sf = SFa + st * kSf + sf_off(tid, 0);
-        const int b0 = (s_begin + i) * 4;
-        if (words && tid < rows) {
-          cp_async4(su32(sf), a.w_scale + (row_g + tid) * (a.K / 32) + b0);
+        if (words && gt < rows) cp_async4(raws + slot * L::kRawWBytes, sp + i * 4);
+      }
+      cp_commit();
+    };
+    // codes 32 seg .. + 15 and + 16 .. + 31 of a row: the first 8 bytes of slots 2 seg and 2 seg + 1
+    const uint32_t d0 = su32(As) + sw128_off(r0, 2 * seg), d1 = su32(As) + sw128_off(r0, 2 * seg + 1);
+    const uint32_t ds = su32(SFa) + sf_off(gt, 0);
+#pragma unroll 1
+    for (int i = grp; i < L::kRawW - kGroups; i += kGroups) copy(i, i);
+    int slot = grp, ahead = L::kRawW - kGroups + grp;
+#pragma unroll 1
+    for (int i = grp; i < n_step; i += kGroups) {
+      copy(i + L::kRawW - kGroups, ahead);
+      if ((ahead += kGroups) >= L::kRawW) ahead -= L::kRawW;
+      cp_wait<L::kRawW / kGroups - 1>();
+      const int st = i % kStages;
+      if (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1)) break;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 v = ld_shared16(raw + slot * L::kRawWBytes + j * 2048);
+        st_shared8(d0 + st * kTileA + j * 4096, v.x, v.y);
+        st_shared8(d1 + st * kTileA + j * 4096, v.z, v.w);
+      }
+      uint32_t sw = 0x7f7f7f7fu;
+      if (gt < rows) {
+        if (words) {
+          sw = ld_shared4(raws + slot * L::kRawWBytes);
         } else {
-          uint32_t w = 0x7f7f7f7fu;
-          if (tid < rows) {
-            const uint8_t* src = a.w_scale + (row_g + tid) * (a.K / 32) + b0;
-            w = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) w |= (b0 + b < a.K / 32 ? static_cast<uint32_t>(__ldg(src + b)) : 0x7fu) << (8 * b);
-          }
-          *reinterpret_cast<uint32_t*>(sf) = w;
+          const int nb = a.K / 32 - (s_begin + i) * 4;  // scale bytes left in the row
+          for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(sp + i * 4 + b)) << (8 * b);
         }
       }
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead) : "memory");
-      if (i >= kAhead) {
-        fence_async_smem();
-        mbar_arrive(su32(&full[(i - kAhead) % kStages]));
-      }
+      st_shared4(ds + st * kSf, sw);
+      fence_async_smem();
+      mbar_arrive(su32(&full[st]));
+      if ((slot += kGroups) >= L::kRawW) slot -= L::kRawW;
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-  } else if (warp < 8) {
-    // ---------------- x: B's columns
-    const int xt = tid - 128;
+  } else if (warp < kMmaWarp) {
+    // ---------------- x: B's columns, copied kRawX - 1 steps ahead.  Four lanes share a 32-value block of
+    // a BF16 row (8 values, 16 bytes each), two a block of MXFP8 codes.
+    constexpr int kLpr = kMx ? 8 : 16;        // lanes per row
+    constexpr int kXTok = 128 / kLpr;         // rows at once
+    const int grp = (warp >> 2) - kGroups, xt = tid & 127, xc = xt % kLpr, xb = xc / (kLpr / 4), t0 = xt / kLpr;
     const int64_t ldx = static_cast<int64_t>(a.G) * a.K;
-    bool ok = true;
-    for (int i = 0; ok && i < n_step; ++i) {
+    const int64_t x0 = (n0 + t0) * ldx + static_cast<int64_t>(g) * a.K + static_cast<int64_t>(s_begin) * kK + xc * (kK / kLpr);
+    const bool words = a.K % 128 == 0, scaler = xc % (kLpr / 4) == 0;
+    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + 128 * L::kU * 16 + t0 * 4;
+    auto copy = [&](int i, int slot) {
+      if (i < n_step) {
+        const bool in = (s_begin + i) * 4 + xb < a.K / 32;
+        const int64_t at = x0 + static_cast<int64_t>(i) * kK;
+#pragma unroll
+        for (int m = 0; m < L::kU; ++m) {
+          const bool v = in && t0 + kXTok * m < n_tok;
+          const int64_t am = at + kXTok * m * ldx;
+          cp_async16z(raw + slot * L::kRawXBytes + m * 2048, v ? static_cast<const uint8_t*>(a.x) + am * (kMx ? 1 : 2) : a.x, v);
+          if (kMx && words && xc == 0 && v) cp_async4(raws + slot * L::kRawXBytes + m * kXTok * 4, a.x_scale + am / 32);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll 1
+    for (int i = grp; i < L::kRawX - kGroups; i += kGroups) copy(i, i);
+    int slot = grp, ahead = L::kRawX - kGroups + grp;
+#pragma unroll 1
+    for (int i = grp; i < n_step; i += kGroups) {
+      copy(i + L::kRawX - kGroups, ahead);
+      if ((ahead += kGroups) >= L::kRawX) ahead -= L::kRawX;
+      cp_wait<L::kRawX / kGroups - 1>();
+      if (kMx) __syncwarp();  // a row's scale word is copied by its first lane
       const int st = i % kStages;
-      if (i >= kStages) ok = wait(&empty[st], ((i / kStages) - 1) & 1);
-      if (!ok) break;
-      uint8_t* Bt = Bs + st * N * kK;
-      uint8_t* sf = SFb + st * kSf;
-      const int kb = (s_begin + i) * 4;  // first 32-block of the step
-      for (int u = xt; u < n_tok * 4; u += 128) {
-        const int t = u >> 2, b = u & 3;
-        const bool in = kb + b < a.K / 32;
-        const int64_t at = (n0 + t) * ldx + static_cast<int64_t>(g) * a.K + (kb + b) * 32;
+      if (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1)) break;
+      const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
+#pragma unroll 1
+      for (int m = 0; m < L::kU; ++m) {
+        const int t = t0 + kXTok * m;
+        if (t - (lane / kLpr) >= n_tok) break;  // the same for every lane
+        const uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * 2048);
         if constexpr (kMx) {
-          uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-          uint8_t sc = 127;
-          if (in) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + at);
-            v0 = __ldg(p);
-            v1 = __ldg(p + 1);
-            sc = __ldg(a.x_scale + at / 32);
+          if (t >= n_tok) continue;
+          st_shared16(Bt + sw128_off(t, xc), v);
+          if (scaler) {
+            uint32_t sc = 127;
+            if (words) sc = ld_shared4(raws + slot * L::kRawXBytes + m * kXTok * 4) >> (8 * xb);
+            else if ((s_begin + i) * 4 + xb < a.K / 32) sc = __ldg(a.x_scale + (x0 + kXTok * m * ldx + static_cast<int64_t>(i) * kK) / 32);
+            st_shared1(sf + sf_off(t, xb), sc);
           }
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t, 2 * b)) = v0;
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t, 2 * b + 1)) = v1;
-          sf[sf_off(t, b)] = sc;
         } else {
-          uint32_t w[16];
-          float amax = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at) + j);
-            w[4 * j] = v.x;
-            w[4 * j + 1] = v.y;
-            w[4 * j + 2] = v.z;
-            w[4 * j + 3] = v.w;
-          }
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          // the block's largest magnitude as BF16 bits (an infinity's or a NaN's are larger still)
+          uint32_t mb = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+          mb = max(mb & 0xffffu, mb >> 16);
+          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
           bool inf = false;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(finite_abs(lo), finite_abs(hi)));
-            inf |= !(fabsf(lo) < INFINITY) | !(fabsf(hi) < INFINITY);
+          if (__any_sync(0xffffffffu, mb >= 0x7f80u)) {  // the largest finite value, then
+            float amax = 0.f;
+            for (int j = 0; j < 4; ++j) {
+              amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[j] << 16)), finite_abs(__uint_as_float(w[j] & 0xffff0000u))));
+              inf |= ((w[j] & 0x7f80u) == 0x7f80u) | ((w[j] & 0x7f800000u) == 0x7f800000u);
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            mb = __float_as_uint(amax) >> 16;
           }
           // 16 / X's exponent has to fit E8M0 too, and 2^-e FP32
-          const int e = amax > 0.f ? min(max(e4m3_scale_exp(amax), -120), 119) : 0;
+          const int e = mb > 0 ? min(max(e4m3_scale_exp(__uint_as_float(mb << 16)), -120), 119) : 0;
           const float f = pow2f(-e);
-          uint32_t hi4[8], lo4[8];
+          uint16_t h8[4], l8[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float v[4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              v[2 * q] = __uint_as_float(w[2 * j + q] << 16) * f;
-              v[2 * q + 1] = __uint_as_float(w[2 * j + q] & 0xffff0000u) * f;
-            }
-            hi4[j] = e4m3x4(v[0], v[1], v[2], v[3]);
-            const float2 h0 = e4m3x2_to_f32x2(static_cast<uint16_t>(hi4[j] & 0xffffu));
-            const float2 h1 = e4m3x2_to_f32x2(static_cast<uint16_t>(hi4[j] >> 16));
-            lo4[j] = e4m3x4((v[0] - h0.x) * 16.f, (v[1] - h0.y) * 16.f, (v[2] - h1.x) * 16.f, (v[3] - h1.y) * 16.f);
+          for (int j = 0; j < 4; ++j) {
+            // x / X in F16: exact, or below 2^-17, where both terms are 0 anyway
+            const __half2 y = __floats2half2_rn(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+            h8[j] = f16x2_to_e4m3x2(y);
+            l8[j] = f16x2_to_e4m3x2(__hmul2(__hsub2(y, e4m3x2_to_f16x2(h8[j])), __float2half2_rn(16.f)));  // exact before the rounding
           }
-          // an infinity has no E4M3 code; like a NaN it makes the outputs NaN
-          if (inf) hi4[0] |= 0x7fu;
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t, 2 * b)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t, 2 * b + 1)) = make_uint4(hi4[4], hi4[5], hi4[6], hi4[7]);
-          const int t2 = kTok + t;
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t2, 2 * b)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-          *reinterpret_cast<uint4*>(Bt + sw128_off(t2, 2 * b + 1)) = make_uint4(lo4[4], lo4[5], lo4[6], lo4[7]);
-          sf[sf_off(t, b)] = static_cast<uint8_t>(e + 127);
-          sf[sf_off(t2, b)] = static_cast<uint8_t>(e - 4 + 127);
+          if (t >= n_tok) continue;
+          uint32_t h0 = h8[0] | static_cast<uint32_t>(h8[1]) << 16;
+          if (inf) h0 |= 0x7fu;  // an infinity has no E4M3 code; like a NaN it makes the outputs NaN
+          const uint32_t off = sw128_off(t, xc >> 1) + (xc & 1) * 8;
+          st_shared8(Bt + off, h0, h8[2] | static_cast<uint32_t>(h8[3]) << 16);
+          st_shared8(Bt + off + kTok * 128, l8[0] | static_cast<uint32_t>(l8[1]) << 16, l8[2] | static_cast<uint32_t>(l8[3]) << 16);
+          if (scaler) {
+            st_shared1(sf + sf_off(t, xb), e + 127);
+            st_shared1(sf + sf_off(kTok + t, xb), e - 4 + 127);
+          }
         }
       }
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
+      if ((slot += kGroups) >= L::kRawX) slot -= L::kRawX;
     }
-  } else if (lane == 0) {
-    // ---------------- MMAs: E2M1 x E4M3, E8M0 scales, FP32 accumulate
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  } else {
+    // ---------------- MMAs: E2M1 x E4M3, E8M0 scales, FP32 accumulate; the warp stays together and one
+    // lane issues, which keeps the descriptors in uniform registers
+    const bool one = elect_one();
     const uint32_t idesc0 = (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
                             (static_cast<uint32_t>(kM >> 4) << 24);
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n_step; ++i) {
       const int st = i % kStages;
-      ok = wait(&full[st], (i / kStages) & 1);
+      ok = __all_sync(0xffffffffu, wait(&full[st], (i / kStages) & 1));
       if (!ok) break;
       fence_after();
       const uint32_t sfa = tm + N + 4u * (i & 1), sfb = tm + N + 8 + 4u * (i & 1);
-      tmem_scales(sfa, SFa + st * kSf);
-      tmem_scales(sfb, SFb + st * kSf);
-      const uint32_t ab = su32(As + st * kTileA), bb = su32(Bs + st * N * kK);
+      const uint64_t ad = sw128_desc(su32(As + st * kTileA)), bd = sw128_desc(su32(Bs + st * N * kK));
+      if (one) {
+        tmem_scales(sfa, SFa + st * kSf);
+        tmem_scales(sfb, SFb + st * kSf);
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k) {
-        const uint32_t idesc = idesc0 | (k << 29) | (k << 4);
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(tm),
-            "l"(sw128_desc(ab + k * 32)), "l"(sw128_desc(bb + k * 32)), "r"(idesc), "r"(static_cast<uint32_t>(i > 0 || k > 0)),
-            "r"(sfa | (k << 30)), "r"(sfb | (k << 30)));
+        for (uint32_t k = 0; k < 4; ++k) {
+          const uint32_t idesc = idesc0 | (k << 29) | (k << 4);
+          asm volatile(
+              "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+              "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(tm),
+              "l"(ad + k * 2), "l"(bd + k * 2), "r"(idesc), "r"(static_cast<uint32_t>(i > 0 || k > 0)),
+              "r"(sfa | (k << 30)), "r"(sfb | (k << 30)));
+        }
+        mma_commit(su32(&empty[st]));
       }
-      mma_commit(su32(&empty[st]));
     }
-    mma_commit(su32(&done));
-    // every MMA complete before shared and tensor memory are used again (finite on the hardware)
-    if (!ok)
-      for (long it = 0; it < kSpin && !mbar_test(su32(&done), 0); ++it) {
-      }
+    if (one) {
+      mma_commit(su32(&done));
+      // every MMA complete before shared and tensor memory are used again (finite on the hardware)
+      if (!ok)
+        for (long it = 0; it < kSpin && !mbar_test(su32(&done), 0); ++it) {
+        }
+    }
   }
   __syncwarp();
 
@@ -296,10 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
     if (a.out_fmt == LC_FMT_F32) static_cast<float*>(a.y)[at] = v;
     else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(v);
   };
+  if (split > 1) {
+    // no CTA of the cluster reads its staged codes any more: partial sums can go there
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp < 4) {
     fence_after();
-#pragma unroll
-    for (int t0 = 0; t0 < kTok; t0 += 8) {
+    int own = 0, place = rank;  // of row t: the CTA that adds it up, this rank's place there
+#pragma unroll 1
+    for (int t0 = 0; t0 < n_tok; t0 += 8) {
       uint32_t v[8], w[8];
       asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
                    : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
@@ -314,25 +409,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
         const int t = t0 + j;
         float y = __uint_as_float(v[j]);
         if constexpr (!kMx) y += __uint_as_float(w[j]);
-        if (split > 1) part[t * kM + tid] = y;
-        else if (ok && t < n_tok && tid < rows) store(t, tid, y);
+        if (split > 1) {
+          if (t < n_tok) st_cluster_f32(su32(part + place * kM + tid), own, y);
+          if (++own == split) {
+            own = 0;
+            place += split;
+          }
+        } else if (ok && t < n_tok && tid < rows) store(t, tid, y);
       }
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tm, kCols);
+  if (warp == kMmaWarp) tmem_dealloc(tm, kCols);
   if (split > 1) {
-    cluster_sync();  // every partial tile is written
-    // this CTA's share of the rows of x, summed over the ranks in order
-    for (int u = tid; u < n_tok * kM; u += kThreads) {
-      const int t = u / kM, r = u % kM;
-      if (t % split != rank || r >= rows) continue;
-      float y = 0.f;
-      for (int p = 0; p < split; ++p) y += ld_cluster_f32(su32(part + u), p);
-      store(t, r, y);
+    cluster_arrive();
+    cluster_wait();  // every partial tile is in place
+    // this CTA's share of the rows of x (t % split == rank), summed over the ranks in order
+    const int items = (n_tok - rank + split - 1) / split * kM;
+    for (int u = tid; u < items; u += kThreads) {
+      const int q = u / kM, r = u % kM;
+      float y = part[q * split * kM + r];
+      for (int p = 1; p < split; ++p) y += part[(q * split + p) * kM + r];
+      if (r < rows) store(q * split + rank, r, y);
     }
-    cluster_sync();  // and read by its peers before it goes
   }
 }
 
@@ -341,8 +441,8 @@ namespace {
 template <int N, bool kMx>
 cudaError_t launch_w4(const lc_w4_proj_args& a, int split, int tiles_g, cudaStream_t st) {
   constexpr int kTok = kMx ? N : N / 2;
-  constexpr size_t smem = static_cast<size_t>(W4Ring<N>::kStages) * W4Ring<N>::kBytes + 1024;
-  static_assert(smem <= 227 * 1024 - 512 && static_cast<size_t>(kTok) * kM * 4 <= smem, "shared memory");
+  constexpr size_t smem = W4Smem<N, kMx>::kBytes;
+  static_assert(smem <= 227 * 1024 - 512, "shared memory");
   const dim3 grid(static_cast<unsigned>(a.G * tiles_g * split), static_cast<unsigned>((a.n_q + kTok - 1) / kTok));
   const cudaError_t e = cudaFuncSetAttribute(k_w4_proj<N, kMx>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -356,12 +456,16 @@ cudaError_t launch_w4_proj(const lc_w4_proj_args& a, cudaStream_t st) {
   const int tiles_g = (a.d_g + kM - 1) / kM;
   const int64_t tiles = static_cast<int64_t>(a.G) * tiles_g;
   const int n_sub = (a.K + kK - 1) / kK;
-  // CTAs that share a tile's inputs: the power of two (up to 8, at least 2 steps each) that leaves
-  // the fewest rounds of whole tiles on the multiprocessors
+  // CTAs that share a tile's inputs (up to 8, at least 2 steps each): the number whose rounds of CTAs
+  // cost least, where a CTA takes as long to start and end as kFixed steps, and `join` more in a cluster
+  constexpr int kFixed = 10;
+  const int join = 4 + std::min(a.n_q, kMaxTok) / 4;
+  const int64_t rows_y = (a.n_q + kMaxTok - 1) / kMaxTok;
   int split = 1;
-  double best = 1e30;
-  for (int s = 1; s <= 8 && (s == 1 || n_sub >= 2 * s); s *= 2) {
-    const double cost = static_cast<double>((tiles * s + sm_count() - 1) / sm_count()) / s + 0.01 * s;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= 8 && (s == 1 || n_sub >= 2 * s); ++s) {
+    const int64_t waves = (tiles * rows_y * s + sm_count() - 1) / sm_count();
+    const int64_t cost = waves * (kFixed + (s > 1 ? join : 0) + (n_sub + s - 1) / s);
     if (cost < best) {
       best = cost;
       split = s;

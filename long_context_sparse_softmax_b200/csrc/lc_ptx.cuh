@@ -128,6 +128,13 @@ __device__ __forceinline__ uint32_t sw128_off(int r, int j) { return r * 128 + (
 __device__ __forceinline__ uint32_t sw64_off(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
 // ---------------------------------------------------------------- tcgen05 MMAs
+// true in one lane of the (converged) warp; a branch on it leaves the other registers warp-uniform
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // D (tensor memory) = A * B (+ D if acc): kind::f16 (BF16 / F16 operands)
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
