@@ -508,8 +508,8 @@ lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);
  * run on the block-scaled tensor cores (FP32 accumulation) on the caller's weight bytes; a
  * BF16 row is split there into two E4M3 terms, exact for values down to 2^-15 of the largest
  * of their 32-value block and within 2^-22 of that largest value below.  A NaN or an infinity
- * in a BF16 row makes the row's outputs of that group NaN.  Each 64 rows of x read the
- * weights once: for many rows use a 16-bit product instead.
+ * in a BF16 row makes the row's outputs of that group NaN.  Each 32 rows of BF16 x (64 of
+ * MXFP8) read the weights once: for many rows use a 16-bit product instead.
  * ------------------------------------------------------------------------------- */
 typedef struct lc_w4_proj_args {
   int32_t n_q;             /* rows of x */

@@ -19,8 +19,6 @@
 // multiprocessors; the partial tiles meet in distributed shared memory and are added in rank
 // order, so the result does not depend on timing.  Every mbarrier wait is bounded
 // (LC_DEV_TIMEOUT).
-#include <algorithm>
-
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
 #include "lc_ptx.cuh"
@@ -33,29 +31,29 @@ constexpr int kM = 128;                 // outputs per tile
 constexpr int kK = 128;                 // inputs per step
 constexpr int kTileA = kM * kK;         // bytes of A in shared memory (padded codes)
 constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 rows of 4 words
-constexpr int kGroups = 2;               // groups of 4 warps that take steps in turn: for the weights, and for x
-constexpr int kMmaWarp = 8 * kGroups;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+// warps by role
+constexpr int kTurns = 2;               // warps of a role that take steps in turn: divides kStages, so that a stage
+                                        // always has the same ones and no barrier is waited for a round too early
+constexpr int kXT = 256;                // threads of a turn that turn x into B's columns
+constexpr int kWarpX = 4 * kTurns, kWarpLw = kWarpX + kXT / 32 * kTurns, kWarpLx = kWarpLw + 2, kWarpMma = kWarpLx + 2;
+constexpr int kThreads = 32 * (kWarpMma + kTurns);
 constexpr long kSpin = 1L << 20;  // a few seconds
-constexpr int kMaxTok = 64;             // rows of x per CTA
 
 // shared memory for N columns of B: kRawW steps of codes and scale words as they come from memory,
 // kRawX steps of x, and kStages steps in the tensor core's layout
 template <int N, bool kMx>
 struct W4Smem {
   static constexpr int kTok = kMx ? N : N / 2;
-  static constexpr int kU = kMx ? kTok / 16 : kTok / 8;   // 16-byte units of x per thread of a group and step
-  static constexpr int kStages = N <= 16 ? 6 : N <= 32 ? 5 : N <= 64 ? 4 : 3;
-  static constexpr int kRawX = N <= 64 ? 6 : 4;           // multiples of kGroups
-  static constexpr int kRawW = N <= 64 ? 8 : 6;
+  static constexpr int kUnits = kTok * (kMx ? 8 : 16);    // 16-byte units of x per step
+  static constexpr int kStages = 4;
+  static constexpr int kRawX = 6;
+  static constexpr int kRawW = 8;
   static constexpr int kStage = kTileA + N * kK + 2 * kSf;
   static constexpr int kRawWBytes = kM * kK / 2 + kM * 4;
-  static constexpr int kRawXBytes = 128 * kU * 16 + (kMx ? kTok * 4 : 0);
+  static constexpr int kRawXBytes = kUnits * 16 + (kMx ? kTok * 4 : 0);
   static constexpr int kRing = kStages * kStage, kW = kRawW * kRawWBytes, kX = kRawX * kRawXBytes;
-  // a CTA's share of the joined rows is (n_tok + split - 1) / split rows of `split` partial sums; it lies
-  // where the codes were
-  static constexpr int kPart = (kTok + 7) * kM * 4;
-  static constexpr int kBytes = kRing + (kW > kPart ? kW : kPart) + kX + 1024;
+  static constexpr int kBytes = kRing + kW + kX + 1024;
+  static_assert(kStages % kTurns == 0 && kTok * kM * 4 <= kW, "turns, partial sums");
 };
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
@@ -64,10 +62,9 @@ __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+// this thread's copies so far arrive on `bar` once complete
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
@@ -101,18 +98,31 @@ __device__ __forceinline__ void tmem_scales(uint32_t taddr, const void* smem) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(d));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
 // byte of row r, 32-value block b of a scale block
 __device__ __forceinline__ int sf_off(int r, int b) { return (r & 31) * 16 + (r >> 5) * 4 + b; }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint16_t f16x2_to_e4m3x2(__half2 v) {
   return __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint16_t v) { return __half2(__nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3)); }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v) {
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
   uint32_t r;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(r), "f"(v) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
@@ -124,7 +134,8 @@ template <int N, bool kMx>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int split, int tiles_g) {
   using L = W4Smem<N, kMx>;
   constexpr int kStages = L::kStages, kTok = L::kTok;
-  constexpr uint32_t kCols = N + 16 <= 32 ? 32 : N + 16 <= 64 ? 64 : N + 16 <= 128 ? 128 : 256;
+  constexpr int kAcc = N + 16;                    // tensor-memory columns of an issuing warp: sums, scales
+  constexpr uint32_t kCols = kTurns * kAcc <= 64 ? 64 : kTurns * kAcc <= 128 ? 128 : kTurns * kAcc <= 256 ? 256 : 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* As = smem;                              // [kStages][kTileA]
@@ -133,11 +144,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   uint8_t* SFb = SFa + kStages * kSf;              // [kStages][kSf]
   uint8_t* Xr = SFb + kStages * kSf;               // [kRawX][kRawXBytes]
   uint8_t* Wr = Xr + L::kX;                        // [kRawW][kRawWBytes]
-  // partial tiles of a cluster: the row's place in the share of the CTA that adds it up, rank, output
-  float* part = reinterpret_cast<float*>(Wr);
+  float* part = reinterpret_cast<float*>(Wr);      // after the last step: the partial tile of a cluster's CTA [kTok][kM]
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
+  __shared__ __align__(8) uint64_t wfull[L::kRawW], wempty[L::kRawW], xfull[L::kRawX], xempty[L::kRawX];
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = static_cast<int>(blockIdx.x) % split;
@@ -162,14 +173,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
     return false;
   };
 
-  if (warp == kMmaWarp) tmem_alloc(su32(&s_tmem), kCols);
+  if (warp == kWarpMma) tmem_alloc(su32(&s_tmem), kCols);
   if (tid == 0) {
     s_abort = 0;
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(su32(&full[i]), 256);
+      mbar_init(su32(&full[i]), 128 + kXT);
       mbar_init(su32(&empty[i]), 1);
     }
-    mbar_init(su32(&done), 1);
+    for (int i = 0; i < L::kRawW; ++i) {
+      mbar_init(su32(&wfull[i]), 64);
+      mbar_init(su32(&wempty[i]), 128);
+    }
+    for (int i = 0; i < L::kRawX; ++i) {
+      mbar_init(su32(&xfull[i]), 64);
+      mbar_init(su32(&xempty[i]), kXT);
+    }
+    mbar_init(su32(&done), kTurns);
     fence_mbar_init();
   }
   // columns of B without a row of x stay zero (scale 2^0) in every stage
@@ -181,122 +200,155 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   fence_after();
   const uint32_t tm = s_tmem;
 
-  if (warp < 4 * kGroups) {
-    // ---------------- the weights: 16 bytes (32 codes) of 4 rows a thread and step, copied kRawW - 1
-    // steps ahead into places of the thread's own, then spread.  (Copies of 8 bytes would land in place by
-    // themselves, but took 950 cycles a step.)
+  // The copying warps never meet a proxy fence: it would wait for every copy still in flight (1000 cycles
+  // a step).  The converting warps, which need one before the tensor core reads, copy nothing.
+  const bool words = a.K % 128 == 0;  // a row's four scale bytes of a step are one aligned word
+  auto copies_arrive = [&](uint32_t bar) {
+    if (words) {
+      cp_arrive(bar);
+    } else {  // scale words were stored, too
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+      mbar_arrive(bar);
+    }
+  };
+  if (warp >= kWarpLw && warp < kWarpLx) {
+    // ---------------- copies of the weights: 16 bytes (32 codes) of 8 rows a thread and step
     const int64_t row_g = static_cast<int64_t>(g) * a.d_g + c0;
-    const int grp = warp >> 2, gt = tid & 127;
-    const int seg = lane & 3, r0 = (warp & 3) * 8 + (lane >> 2);  // rows r0 + 32 j
-    const bool words = a.K % 128 == 0;  // a row's four scale bytes of a step are one aligned word
+    const int lt = tid & 63, seg = lt & 3, r0 = lt >> 2;  // rows r0 + 16 j
     const uint8_t* wp = a.w + (row_g + r0) * (a.K / 2) + static_cast<int64_t>(s_begin) * (kK / 2) + seg * 16;
-    const int64_t r32 = static_cast<int64_t>(a.K) * 16;      // 32 rows further
-    const uint8_t* sp = a.w_scale + (row_g + gt) * (a.K / 32) + s_begin * 4;
-    const uint32_t raw = su32(Wr) + gt * 16, raws = su32(Wr) + kM * kK / 2 + gt * 4;
-    auto copy = [&](int i, int slot) {
-      if (i < n_step) {
-        const uint8_t* p = wp + static_cast<int64_t>(i) * (kK / 2);
-        const bool k_in = (s_begin + i) * kK + seg * 32 < a.K;
+    const int64_t r16 = static_cast<int64_t>(a.K) * 8;       // 16 rows further
+    const uint8_t* sp = a.w_scale + (row_g + lt) * (a.K / 32) + s_begin * 4;
+    const uint32_t raw = su32(Wr) + lt * 16, raws = su32(Wr) + kM * kK / 2 + lt * 4;
+    int slot = 0, round = 0;
+#pragma unroll 1
+    for (int i = 0; i < n_step; ++i) {
+      if (round > 0 && !wait(&wempty[slot], (round - 1) & 1)) break;
+      const bool k_in = (s_begin + i) * kK + seg * 32 < a.K;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool v = k_in && r0 + 32 * j < rows;
-          cp_async16z(raw + slot * L::kRawWBytes + j * 2048, v ? p + j * r32 : a.w, v);
-        }
-        if (words && gt < rows) cp_async4(raws + slot * L::kRawWBytes, sp + i * 4);
+      for (int j = 0; j < 8; ++j) {
+        const bool v = k_in && r0 + 16 * j < rows;
+        cp_async16z(raw + slot * L::kRawWBytes + j * 1024, v ? wp + j * r16 : a.w, v);
       }
-      cp_commit();
-    };
-    // codes 32 seg .. + 15 and + 16 .. + 31 of a row: the first 8 bytes of slots 2 seg and 2 seg + 1
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (lt + 64 * h >= rows) continue;
+        const uint8_t* p = sp + h * 64 * static_cast<int64_t>(a.K / 32);
+        if (words) {
+          cp_async4(raws + slot * L::kRawWBytes + h * 256, p);
+        } else {
+          uint32_t sw = 0x7f7f7f7fu;
+          const int nb = a.K / 32 - (s_begin + i) * 4;  // scale bytes left in the row
+          for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(p + b)) << (8 * b);
+          st_shared4(raws + slot * L::kRawWBytes + h * 256, sw);
+        }
+      }
+      copies_arrive(su32(&wfull[slot]));
+      wp += kK / 2;
+      sp += 4;
+      if (++slot == L::kRawW) {
+        slot = 0;
+        ++round;
+      }
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+  } else if (warp < kWarpX) {
+    // ---------------- the weights into A's layout (8-byte copies would land there by themselves, but ran
+    // at a third of the rate): codes 32 seg .. + 15 and + 16 .. + 31 of a row are the first 8 bytes of
+    // slots 2 seg and 2 seg + 1
+    const int wt = tid & 127, seg = wt & 3, r0 = wt >> 2;
+    const uint32_t raw = su32(Wr) + wt * 16, raws = su32(Wr) + kM * kK / 2 + wt * 4;
     const uint32_t d0 = su32(As) + sw128_off(r0, 2 * seg), d1 = su32(As) + sw128_off(r0, 2 * seg + 1);
-    const uint32_t ds = su32(SFa) + sf_off(gt, 0);
+    const uint32_t ds = su32(SFa) + sf_off(wt, 0);
 #pragma unroll 1
-    for (int i = grp; i < L::kRawW - kGroups; i += kGroups) copy(i, i);
-    int slot = grp, ahead = L::kRawW - kGroups + grp;
-#pragma unroll 1
-    for (int i = grp; i < n_step; i += kGroups) {
-      copy(i + L::kRawW - kGroups, ahead);
-      if ((ahead += kGroups) >= L::kRawW) ahead -= L::kRawW;
-      cp_wait<L::kRawW / kGroups - 1>();
-      const int st = i % kStages;
-      if (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1)) break;
+    for (int i = warp >> 2; i < n_step; i += kTurns) {
+      const int st = i % kStages, slot = i % L::kRawW;
+      if (!wait(&wfull[slot], (i / L::kRawW) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint4 v = ld_shared16(raw + slot * L::kRawWBytes + j * 2048);
         st_shared8(d0 + st * kTileA + j * 4096, v.x, v.y);
         st_shared8(d1 + st * kTileA + j * 4096, v.z, v.w);
       }
-      uint32_t sw = 0x7f7f7f7fu;
-      if (gt < rows) {
-        if (words) {
-          sw = ld_shared4(raws + slot * L::kRawWBytes);
-        } else {
-          const int nb = a.K / 32 - (s_begin + i) * 4;  // scale bytes left in the row
-          for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(sp + i * 4 + b)) << (8 * b);
-        }
-      }
-      st_shared4(ds + st * kSf, sw);
+      st_shared4(ds + st * kSf, wt < rows ? ld_shared4(raws + slot * L::kRawWBytes) : 0x7f7f7f7fu);
+      mbar_arrive(su32(&wempty[slot]));
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
-      if ((slot += kGroups) >= L::kRawW) slot -= L::kRawW;
+    }
+  } else if (warp >= kWarpLx && warp < kWarpMma) {
+    // ---------------- copies of x: 16 bytes a lane
+    constexpr int kLpr = kMx ? 8 : 16, kXTok = 64 / kLpr;  // lanes per row, rows at once
+    constexpr int kB = kMx ? 1 : 2;
+    const int xt = tid & 63, xc = xt % kLpr, t0 = xt / kLpr;
+    const int64_t ldx = static_cast<int64_t>(a.G) * a.K;
+    const int64_t at = (n0 + t0) * ldx + static_cast<int64_t>(g) * a.K + static_cast<int64_t>(s_begin) * kK + xc * (kK / kLpr);
+    const uint8_t* xp = static_cast<const uint8_t*>(a.x) + at * kB;   // of the step
+    const uint8_t* sp = kMx ? a.x_scale + at / 32 : nullptr;
+    const int64_t row_x = kXTok * ldx * kB, row_s = kXTok * ldx / 32;
+    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + L::kUnits * 16 + t0 * 4;
+    const int n_it = (n_tok + kXTok - 1) / kXTok;
+    int slot = 0, round = 0;
+#pragma unroll 1
+    for (int i = 0; i < n_step; ++i) {
+      if (round > 0 && !wait(&xempty[slot], (round - 1) & 1)) break;
+      const int nb = a.K / 32 - (s_begin + i) * 4;  // blocks left in the row
+      const bool in = xc / (kLpr / 4) < nb;
+      const uint32_t dst = raw + slot * L::kRawXBytes, dsts = raws + slot * L::kRawXBytes;
+      const uint8_t *p = xp, *q = sp;
+      int t = t0;
+#pragma unroll 2
+      for (int m = 0; m < n_it; ++m) {
+        const bool v = in && t < n_tok;
+        cp_async16z(dst + m * 1024, v ? p : static_cast<const uint8_t*>(a.x), v);
+        if (kMx && xc == 0 && t < n_tok) {
+          if (words) {
+            cp_async4(dsts + m * kXTok * 4, q);
+          } else {
+            uint32_t sw = 0x7f7f7f7fu;
+            for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(q + b)) << (8 * b);
+            st_shared4(dsts + m * kXTok * 4, sw);
+          }
+        }
+        p += row_x;
+        q += row_s;
+        t += kXTok;
+      }
+      copies_arrive(su32(&xfull[slot]));
+      xp += kK * kB;
+      sp += 4;
+      if (++slot == L::kRawX) {
+        slot = 0;
+        ++round;
+      }
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-  } else if (warp < kMmaWarp) {
-    // ---------------- x: B's columns, copied kRawX - 1 steps ahead.  Four lanes share a 32-value block of
-    // a BF16 row (8 values, 16 bytes each), two a block of MXFP8 codes.
-    constexpr int kLpr = kMx ? 8 : 16;        // lanes per row
-    constexpr int kXTok = 128 / kLpr;         // rows at once
-    const int grp = (warp >> 2) - kGroups, xt = tid & 127, xc = xt % kLpr, xb = xc / (kLpr / 4), t0 = xt / kLpr;
-    const int64_t ldx = static_cast<int64_t>(a.G) * a.K;
-    const int64_t x0 = (n0 + t0) * ldx + static_cast<int64_t>(g) * a.K + static_cast<int64_t>(s_begin) * kK + xc * (kK / kLpr);
-    const bool words = a.K % 128 == 0, scaler = xc % (kLpr / 4) == 0;
-    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + 128 * L::kU * 16 + t0 * 4;
-    auto copy = [&](int i, int slot) {
-      if (i < n_step) {
-        const bool in = (s_begin + i) * 4 + xb < a.K / 32;
-        const int64_t at = x0 + static_cast<int64_t>(i) * kK;
-#pragma unroll
-        for (int m = 0; m < L::kU; ++m) {
-          const bool v = in && t0 + kXTok * m < n_tok;
-          const int64_t am = at + kXTok * m * ldx;
-          cp_async16z(raw + slot * L::kRawXBytes + m * 2048, v ? static_cast<const uint8_t*>(a.x) + am * (kMx ? 1 : 2) : a.x, v);
-          if (kMx && words && xc == 0 && v) cp_async4(raws + slot * L::kRawXBytes + m * kXTok * 4, a.x_scale + am / 32);
-        }
-      }
-      cp_commit();
-    };
+  } else if (warp < kWarpLw) {
+    // ---------------- x into B's columns.  Four lanes share a 32-value block of a BF16 row (8 values each),
+    // two a block of MXFP8 codes
+    constexpr int kLpr = kMx ? 8 : 16, kXTok = kXT / kLpr;
+    const int xt = (tid - 32 * kWarpX) % kXT, xc = xt % kLpr, xb = xc / (kLpr / 4), t0 = xt / kLpr;
+    const bool scaler = xc % (kLpr / 4) == 0;
+    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + L::kUnits * 16 + t0 * 4;
 #pragma unroll 1
-    for (int i = grp; i < L::kRawX - kGroups; i += kGroups) copy(i, i);
-    int slot = grp, ahead = L::kRawX - kGroups + grp;
-#pragma unroll 1
-    for (int i = grp; i < n_step; i += kGroups) {
-      copy(i + L::kRawX - kGroups, ahead);
-      if ((ahead += kGroups) >= L::kRawX) ahead -= L::kRawX;
-      cp_wait<L::kRawX / kGroups - 1>();
-      if (kMx) __syncwarp();  // a row's scale word is copied by its first lane
-      const int st = i % kStages;
-      if (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1)) break;
+    for (int i = (warp - kWarpX) / (kXT / 32); i < n_step; i += kTurns) {
+      const int st = i % kStages, slot = i % L::kRawX;
+      if (!wait(&xfull[slot], (i / L::kRawX) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
       const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
-#pragma unroll 1
-      for (int m = 0; m < L::kU; ++m) {
+#pragma unroll 2
+      for (int m = 0; m < (kTok + kXTok - 1) / kXTok; ++m) {
         const int t = t0 + kXTok * m;
         if (t - (lane / kLpr) >= n_tok) break;  // the same for every lane
-        const uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * 2048);
+        const uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * (kXT * 16));
         if constexpr (kMx) {
           if (t >= n_tok) continue;
           st_shared16(Bt + sw128_off(t, xc), v);
-          if (scaler) {
-            uint32_t sc = 127;
-            if (words) sc = ld_shared4(raws + slot * L::kRawXBytes + m * kXTok * 4) >> (8 * xb);
-            else if ((s_begin + i) * 4 + xb < a.K / 32) sc = __ldg(a.x_scale + (x0 + kXTok * m * ldx + static_cast<int64_t>(i) * kK) / 32);
-            st_shared1(sf + sf_off(t, xb), sc);
-          }
+          if (scaler) st_shared1(sf + sf_off(t, xb), ld_shared4(raws + slot * L::kRawXBytes + m * kXTok * 4) >> (8 * xb));
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           // the block's largest magnitude as BF16 bits (an infinity's or a NaN's are larger still)
-          uint32_t mb = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+          uint32_t mb = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+          mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+          mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
           mb = max(mb & 0xffffu, mb >> 16);
-          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-          mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
           bool inf = false;
           if (__any_sync(0xffffffffu, mb >= 0x7f80u)) {  // the largest finite value, then
             float amax = 0.f;
@@ -331,25 +383,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
           }
         }
       }
+      mbar_arrive(su32(&xempty[slot]));
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
-      if ((slot += kGroups) >= L::kRawX) slot -= L::kRawX;
     }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
   } else {
-    // ---------------- MMAs: E2M1 x E4M3, E8M0 scales, FP32 accumulate; the warp stays together and one
-    // lane issues, which keeps the descriptors in uniform registers
+    // ---------------- MMAs: E2M1 x E4M3, E8M0 scales, FP32 accumulate.  Each issuing warp has its own sums
+    // (one thread issues an instruction about every 55 cycles, seven a step); the warp stays together and
+    // one lane issues, which keeps the descriptors in uniform registers
+    const int me = warp - kWarpMma;
+    const uint32_t acc = tm + me * kAcc;
     const bool one = elect_one();
     const uint32_t idesc0 = (5u << 7) | (0u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
                             (static_cast<uint32_t>(kM >> 4) << 24);
     bool ok = true;
 #pragma unroll 1
-    for (int i = 0; i < n_step; ++i) {
+    for (int i = me; i < n_step; i += kTurns) {
       const int st = i % kStages;
       ok = __all_sync(0xffffffffu, wait(&full[st], (i / kStages) & 1));
       if (!ok) break;
       fence_after();
-      const uint32_t sfa = tm + N + 4u * (i & 1), sfb = tm + N + 8 + 4u * (i & 1);
+      const uint32_t sfa = acc + N + 4u * ((i / kTurns) & 1), sfb = acc + N + 8 + 4u * ((i / kTurns) & 1);
       const uint64_t ad = sw128_desc(su32(As + st * kTileA)), bd = sw128_desc(su32(Bs + st * N * kK));
       if (one) {
         tmem_scales(sfa, SFa + st * kSf);
@@ -359,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
           const uint32_t idesc = idesc0 | (k << 29) | (k << 4);
           asm volatile(
               "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-              "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(tm),
-              "l"(ad + k * 2), "l"(bd + k * 2), "r"(idesc), "r"(static_cast<uint32_t>(i > 0 || k > 0)),
+              "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(acc),
+              "l"(ad + k * 2), "l"(bd + k * 2), "r"(idesc), "r"(static_cast<uint32_t>(i > me || k > 0)),
               "r"(sfa | (k << 30)), "r"(sfb | (k << 30)));
         }
         mma_commit(su32(&empty[st]));
@@ -384,55 +438,54 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
     if (a.out_fmt == LC_FMT_F32) static_cast<float*>(a.y)[at] = v;
     else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(v);
   };
-  if (split > 1) {
-    // no CTA of the cluster reads its staged codes any more: partial sums can go there
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-  }
   if (warp < 4) {
     fence_after();
-    int own = 0, place = rank;  // of row t: the CTA that adds it up, this rank's place there
 #pragma unroll 1
     for (int t0 = 0; t0 < n_tok; t0 += 8) {
-      uint32_t v[8], w[8];
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                   : "r"(tm + lane_off + t0));
-      if constexpr (!kMx)
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "r"(tm + lane_off + kTok + t0));
+      // an issuing warp that had no step left its sums unwritten
+      constexpr int kSum = kMx ? kTurns : 2 * kTurns;
+      uint32_t v[kSum][8];
+#pragma unroll
+      for (int q = 0; q < kSum; ++q)
+        tmem_ld8(tm + lane_off + (kMx ? q : q / 2) * kAcc + (kMx ? 0 : (q & 1) * kTok) + t0, v[q]);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int t = t0 + j;
-        float y = __uint_as_float(v[j]);
-        if constexpr (!kMx) y += __uint_as_float(w[j]);
+        float y = __uint_as_float(v[0][j]);
+#pragma unroll
+        for (int q = 1; q < kSum; ++q)
+          if ((kMx ? q : q / 2) < n_step) y += __uint_as_float(v[q][j]);
         if (split > 1) {
-          if (t < n_tok) st_cluster_f32(su32(part + place * kM + tid), own, y);
-          if (++own == split) {
-            own = 0;
-            place += split;
-          }
+          if (t < n_tok) part[t * kM + tid] = y;
         } else if (ok && t < n_tok && tid < rows) store(t, tid, y);
       }
     }
   }
   fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tm, kCols);
+  if (warp == kWarpMma) tmem_dealloc(tm, kCols);
   if (split > 1) {
     cluster_arrive();
     cluster_wait();  // every partial tile is in place
-    // this CTA's share of the rows of x (t % split == rank), summed over the ranks in order
-    const int items = (n_tok - rank + split - 1) / split * kM;
+    // this CTA's share of the rows of x (t % split == rank), 4 outputs a thread, added in the order of ranks
+    const int items = (n_tok - rank + split - 1) / split * (kM / 4);
     for (int u = tid; u < items; u += kThreads) {
-      const int q = u / kM, r = u % kM;
-      float y = part[q * split * kM + r];
-      for (int p = 1; p < split; ++p) y += part[(q * split + p) * kM + r];
-      if (r < rows) store(q * split + rank, r, y);
+      const int t = u / (kM / 4) * split + rank, r = u % (kM / 4) * 4;
+      const uint32_t at = su32(part + t * kM + r);
+      float4 y = ld_cluster_f32x4(at, 0);
+#pragma unroll 4
+      for (int p = 1; p < split; ++p) {
+        const float4 v = ld_cluster_f32x4(at, p);
+        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+      }
+      if (r < rows) store(t, r, y.x);
+      if (r + 1 < rows) store(t, r + 1, y.y);
+      if (r + 2 < rows) store(t, r + 2, y.z);
+      if (r + 3 < rows) store(t, r + 3, y.w);
     }
+    cluster_arrive();
+    cluster_wait();  // and read by the peers before it goes
   }
 }
 
@@ -457,15 +510,15 @@ cudaError_t launch_w4_proj(const lc_w4_proj_args& a, cudaStream_t st) {
   const int64_t tiles = static_cast<int64_t>(a.G) * tiles_g;
   const int n_sub = (a.K + kK - 1) / kK;
   // CTAs that share a tile's inputs (up to 8, at least 2 steps each): the number whose rounds of CTAs
-  // cost least, where a CTA takes as long to start and end as kFixed steps, and `join` more in a cluster
-  constexpr int kFixed = 10;
-  const int join = 4 + std::min(a.n_q, kMaxTok) / 4;
-  const int64_t rows_y = (a.n_q + kMaxTok - 1) / kMaxTok;
+  // cost least, where a CTA takes as long to start and end as kFixed steps, and kJoin more in a cluster
+  constexpr int kFixed = 10, kJoin = 6;
+  const int max_tok = a.in_fmt == LC_FMT_MXFP8 ? 64 : 32;  // rows of x per CTA
+  const int64_t rows_y = (a.n_q + max_tok - 1) / max_tok;
   int split = 1;
   int64_t best = INT64_MAX;
   for (int s = 1; s <= 8 && (s == 1 || n_sub >= 2 * s); ++s) {
     const int64_t waves = (tiles * rows_y * s + sm_count() - 1) / sm_count();
-    const int64_t cost = waves * (kFixed + (s > 1 ? join : 0) + (n_sub + s - 1) / s);
+    const int64_t cost = waves * (kFixed + (s > 1 ? kJoin : 0) + (n_sub + s - 1) / s);
     if (cost < best) {
       best = cost;
       split = s;
@@ -478,8 +531,7 @@ cudaError_t launch_w4_proj(const lc_w4_proj_args& a, cudaStream_t st) {
   }
   if (a.n_q <= 8) return launch_w4<16, false>(a, split, tiles_g, st);
   if (a.n_q <= 16) return launch_w4<32, false>(a, split, tiles_g, st);
-  if (a.n_q <= 32) return launch_w4<64, false>(a, split, tiles_g, st);
-  return launch_w4<128, false>(a, split, tiles_g, st);
+  return launch_w4<64, false>(a, split, tiles_g, st);
 }
 
 }  // namespace lc
