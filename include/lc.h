@@ -496,6 +496,7 @@ typedef struct lc_add_rms_norm_args {
   uint8_t* y_scale;        /* MXFP8: [n_rows, d/32], 4-byte aligned; else unused */
   float eps;
   int32_t reserved;
+  int32_t* status;         /* optional: LC_DEV_TIMEOUT */
 } lc_add_rms_norm_args;
 
 lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);

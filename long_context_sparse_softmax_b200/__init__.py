@@ -108,7 +108,7 @@ class AttnArgs(ctypes.Structure):
 class AddRmsNormArgs(ctypes.Structure):
     _fields_ = [("n_rows", c_int64), ("d", c_int32), ("in_fmt", c_int32), ("x", c_void_p), ("res", c_void_p),
                 ("res_out", c_void_p), ("w", c_void_p), ("w_fmt", c_int32), ("out_fmt", c_int32), ("y", c_void_p),
-                ("y_scale", c_void_p), ("eps", c_float), ("reserved", c_int32)]
+                ("y_scale", c_void_p), ("eps", c_float), ("reserved", c_int32), ("status", c_void_p)]
 
 
 class W4ProjArgs(ctypes.Structure):

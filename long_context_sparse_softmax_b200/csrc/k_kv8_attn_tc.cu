@@ -82,26 +82,6 @@ __device__ __forceinline__ void st_shared4(uint32_t a, uint32_t x, uint32_t y, u
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// pairs of FP32 values (one instruction for two products or sums)
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1,%2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint32_t& x, uint32_t& y, uint64_t m, uint64_t c) {
-  asm("{\n.reg .b64 t;\nmov.b64 t, {%0,%1};\nfma.rn.f32x2 t, t, %2, %3;\nmov.b64 {%0,%1}, t;\n}\n" : "+r"(x), "+r"(y) : "l"(m), "l"(c));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float sum2(uint64_t a) {
-  float x, y;
-  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a));
-  return x + y;
-}
-
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -287,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
             uint32_t* v = y[g / 2] + (g & 1) * 16;
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) fma2(v[j], v[j + 1], fk, off);
+            for (int j = 0; j < 16; j += 2) fma2_regs(v[j], v[j + 1], fk, off);
           }
           if (edge) {
 #pragma unroll

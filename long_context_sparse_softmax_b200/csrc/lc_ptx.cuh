@@ -201,6 +201,42 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// ---------------------------------------------------------------- arithmetic
+// pairs of FP32 values (one instruction for two products or sums)
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1,%2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2_regs(uint32_t& x, uint32_t& y, uint64_t m, uint64_t c) {
+  asm("{\n.reg .b64 t;\nmov.b64 t, {%0,%1};\nfma.rn.f32x2 t, t, %2, %3;\nmov.b64 {%0,%1}, t;\n}\n" : "+r"(x), "+r"(y) : "l"(m), "l"(c));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t a) {
+  float2 v;
+  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(v.x), "=f"(v.y) : "l"(a));
+  return v;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+
 // 2^x (approximate, flush-to-zero), the softmax exponent
 __device__ __forceinline__ float ex2(float x) {
   float y;
