@@ -211,13 +211,26 @@ def __getattr__(name):
     raise AttributeError(name)
 
 
-def _stream_handle(stream) -> c_void_p:
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current torch stream of the current device.  A call's time on the host counts for the
+    shortest kernels: torch's raw query takes 0.2 us, its stream object 3.5 us."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        torch.cuda.init()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+    if _raw_stream:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _stream_handle(stream) -> int:
     if stream is None:
-        import torch
-        return c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return c_void_p(stream)
-    return c_void_p(stream.cuda_stream)
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _make_call(name: str, st):
