@@ -45,12 +45,6 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   return y;
 }
 
-// two E4M3 codes (low 16 bits) -> two F16 values
-__device__ __forceinline__ uint32_t widen2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
-
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
@@ -110,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   if (kv < min(kv_all, a.max_kv) && tid == 0) set_status(a.status, LC_DEV_BAD_BLOCK);
   const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + (row0 + n_row - 1) / geo.g);
   const int n = rg.hi - rg.lo16;
-  const int len = geo.n_split > 1 ? kv8_split_len(n) : n;
-  const int n_split = geo.n_split > 1 ? kv8_n_split(n) : 1;
+  const int len = geo.n_split > 1 ? kv8_split_len(n, c.H_kv) : n;
+  const int n_split = geo.n_split > 1 ? kv8_n_split(n, c.H_kv) : 1;
   if (split >= n_split) return;
   const int k_begin = rg.lo16 + split * len;
   const int k_end = min(rg.hi, k_begin + len);
@@ -246,16 +240,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
         const bool edge = t0 < all_lo || t0 + 16 > all_hi;
         float x[NT][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          float sc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < NT; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
-          for (int k = 0; k < kKS; ++k) {
-            mma16816(sc, widen2(cur.k[0][k]), widen2(cur.k[1][k]), widen2(cur.k[0][k] >> 16), widen2(cur.k[1][k] >> 16),
-                     qf[i][k][0], qf[i][k][1]);
-          }
+        for (int k = 0; k < kKS; ++k) {
+          uint32_t a0, a1, a2, a3;
+          widen4(cur.k[0][k], a0, a2);
+          widen4(cur.k[1][k], a1, a3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[i][j] = fmaf(sc[j], f_row[i][j & 1] * kf, ev);
+          for (int i = 0; i < NT; ++i) mma16816(x[i], a0, a1, a2, a3, qf[i][k][0], qf[i][k][1]);
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[i][j] = fmaf(x[i][j], f_row[i][j & 1] * kf, ev);
         if (edge) {
           const int ka = t0 + g8, kb = ka + 8;
 #pragma unroll
@@ -319,8 +316,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
           // bytes 4q .. 4q + 3 of the thread's dims: tiles 2q, 2q + 1
           const uint32_t lo0 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x5140), lo1 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x7362);
           const uint32_t hi0 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x5140), hi1 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x7362);
-          const uint32_t a0 = widen2(lo0), a1 = widen2(lo0 >> 16), a2 = widen2(hi0), a3 = widen2(hi0 >> 16);
-          const uint32_t b0 = widen2(lo1), b1 = widen2(lo1 >> 16), b2 = widen2(hi1), b3 = widen2(hi1 >> 16);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          widen4(lo0, a0, a1);
+          widen4(hi0, a2, a3);
+          widen4(lo1, b0, b1);
+          widen4(hi1, b2, b3);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             mma16816(o[i][2 * q], a0, a1, a2, a3, pf[i][0], pf[i][1]);
@@ -394,66 +394,104 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   }
 }
 
-// Joins the splits of each row: one warp per (query, head), splits in order.
+// Joins the splits of each row: a CTA per (query, head), its warps take splits in turn (eight at a
+// time in flight) and meet in shared memory.
+constexpr int kCombineWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo,
-                                                     const float* __restrict__ ws_o, const float2* __restrict__ ws_ml) {
+__global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo, const float* __restrict__ ws_o,
+                                                                    const float2* __restrict__ ws_ml) {
+  constexpr int kE = D / 32;
+  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
+  __shared__ float s_o[kCombineWarps][D];
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t orow = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (orow >= static_cast<int64_t>(a.n_q) * a.H) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t orow = blockIdx.x;
   const int q = static_cast<int>(orow / a.H), head = static_cast<int>(orow % a.H);
   if (q < __ldg(a.q_start) || q >= __ldg(a.q_start + a.num_seqs)) return;
   const int s = seq_of_query(a.q_start, a.num_seqs, q);
   const int q0 = __ldg(a.q_start + s), p0 = __ldg(a.q_pos0 + s);
   const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
   if (q - q0 >= nq) return;
-  // the range of the row tile that held this row
-  const int rr = (q - q0) * geo.g + head % geo.g;
-  const int row0 = rr / geo.rows * geo.rows;
-  const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + geo.rows, static_cast<int64_t>(nq) * geo.g)) - 1;
-  const int kv = min(min(__ldg(a.kv_len + s), a.max_kv), a.cache.table_cols * a.cache.bt);
-  const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row1 / geo.g);
-  const int n_split = geo.tc ? geo.n_split : kv8_n_split(rg.hi - rg.lo16);
+  int n_split = geo.n_split;
+  if (!geo.tc) {
+    // the range of the row tile that held this row
+    const int rr = (q - q0) * geo.g + head % geo.g;
+    const int row0 = rr / geo.rows * geo.rows;
+    const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + geo.rows, static_cast<int64_t>(nq) * geo.g)) - 1;
+    const int kv = min(min(__ldg(a.kv_len + s), a.max_kv), a.cache.table_cols * a.cache.bt);
+    const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row1 / geo.g);
+    n_split = kv8_n_split(rg.hi - rg.lo16, a.cache.H_kv);
+  }
   if (n_split <= 1) return;
   const float2* ml = ws_ml + orow * geo.n_split;
-  float M = -INFINITY;
-  for (int i = lane; i < n_split; i += 32) M = fmaxf(M, ml[i].x);
-  M = warp_max(M);
-  constexpr int kE = D / 32;
-  float acc[kE];
+  const float* po = ws_o + orow * geo.n_split * D + lane * kE;
+  // each warp on its own first: it needs no one else's maximum
+  float M = -INFINITY, L = 0.f, acc[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) acc[e] = 0.f;
-  float L = 0.f;
-  const float* po = ws_o + orow * geo.n_split * D + lane * kE;
-#pragma unroll 4
-  for (int i = 0; i < n_split; ++i) {
-    const float2 x = ml[i];
-    if (x.x == -INFINITY && x.y == 0.f) continue;  // saw no key
-    const float f = ref_factor(x.x, M);
-    L = fmaf(x.y, f, L);
-    float v[kE];
-    if constexpr (kE == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * D);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(i) * D);
-      v[0] = t.x; v[1] = t.y;
-    }
+  for (int i0 = warp; i0 < n_split; i0 += 8 * kCombineWarps) {
+    float2 x[8];
+    float v[8][kE];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[e] = fmaf(v[e], f, acc[e]);
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kCombineWarps;
+      x[j] = make_float2(-INFINITY, 0.f);
+      if (i < n_split) {
+        x[j] = ml[i];
+        if constexpr (kE == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * D);
+          v[j][0] = t.x; v[j][1] = t.y; v[j][2] = t.z; v[j][3] = t.w;
+        } else {
+          const float2 t = *reinterpret_cast<const float2*>(po + static_cast<int64_t>(i) * D);
+          v[j][0] = t.x; v[j][1] = t.y;
+        }
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, x[j].x);
+    const float f0 = ref_factor(M, m);
+    M = m;
+    L *= f0;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (x[j].x == -INFINITY && x[j].y == 0.f) continue;  // saw no key
+      const float f = ref_factor(x[j].x, M);
+      L = fmaf(x[j].y, f, L);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[e] = fmaf(v[j][e], f, acc[e]);
+    }
+  }
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) s_o[warp][lane * kE + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  M = s_m[0];
+#pragma unroll
+  for (int w = 1; w < kCombineWarps; ++w) M = fmaxf(M, s_m[w]);
+  L = 0.f;
+  float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    if (s_m[w] == -INFINITY && s_l[w] == 0.f) continue;
+    const float f = ref_factor(s_m[w], M);
+    L = fmaf(s_l[w], f, L);
+    const float2 t = *reinterpret_cast<const float2*>(&s_o[w][2 * threadIdx.x]);
+    o0 = fmaf(t.x, f, o0);
+    o1 = fmaf(t.y, f, o1);
   }
   float lse;
   const float f = kv8_finish(M, L, a.sink, head, &lse);
-  uint32_t w[kE / 2];
-#pragma unroll
-  for (int e = 0; e < kE / 2; ++e)
-    w[e] = static_cast<uint32_t>(f32_to_bf16_bits(f == 0.f ? 0.f : acc[2 * e] * f)) |
-           (static_cast<uint32_t>(f32_to_bf16_bits(f == 0.f ? 0.f : acc[2 * e + 1] * f)) << 16);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D + lane * kE);
-#pragma unroll
-  for (int e = 0; e < kE / 2; ++e) out[e] = w[e];
-  if (a.lse && lane == 0) a.lse[orow] = lse;
+  reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * D)[threadIdx.x] =
+      static_cast<uint32_t>(f32_to_bf16_bits(o0 * f)) | (static_cast<uint32_t>(f32_to_bf16_bits(o1 * f)) << 16);
+  if (a.lse && threadIdx.x == 0) a.lse[orow] = lse;
 }
 
 namespace {
@@ -478,9 +516,7 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
     const int64_t fill = sm_count() / ctas;
     geo.n_split = static_cast<int>(max(int64_t{1}, min(fill, static_cast<int64_t>(n) / 512)));
   } else {
-    // the split length is 256 up to 32768 keys and n / 128 (rounded up) above: at most 128 splits
-    // below 2^20 keys, then 8192 keys each
-    geo.n_split = n <= kKv8MinSplit * kKv8Splits ? kv8_n_split(n) : max(kKv8Splits, kv8_n_split(n));
+    geo.n_split = kv8_split_bound(n, a.cache.H_kv);
   }
   return geo;
 }
@@ -502,7 +538,7 @@ cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t s
   if (geo.n_split == 1) return cudaGetLastError();
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, true, 1, a, geo,
+  return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>(rows)), dim3(32 * kCombineWarps), 0, st, true, 1, a, geo,
                    static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));
 }
 

@@ -37,16 +37,28 @@ __device__ __forceinline__ Kv8Range kv8_range(int kv, int W, int p_first, int p_
   return r;
 }
 
-// Split of n keys over CTAs: `len` keys each.  A function of the row's own key count alone, so a
-// sequence's result does not depend on the batch it is in.
-constexpr int kKv8MinSplit = 256, kKv8MaxSplit = 8192, kKv8Splits = 128;
-__host__ __device__ __forceinline__ int kv8_split_len(int n) {
-  const int want = ((n + kKv8Splits - 1) / kKv8Splits + 63) / 64 * 64;
-  return want < kKv8MinSplit ? kKv8MinSplit : want > kKv8MaxSplit ? kKv8MaxSplit : want;
+// Split of n keys over CTAs: `len` keys each.  A function of the row's own key count and of the
+// shared heads alone, so a sequence's result does not depend on the batch it is in.  256 keys where
+// a sequence is short and its latency counts, 512 above 4096 keys (a split costs 8 partial rows of
+// D FP32 values next to 2 D bytes a key: 3 %), and from most_splits * 512 keys on as many as fill
+// the device with one sequence (576 CTAs: 4 on each multiprocessor), up to 8192 keys each.
+constexpr int kKv8MaxSplit = 8192;
+__host__ __device__ __forceinline__ int kv8_most_splits(int H_kv) { return H_kv >= 8 ? 72 : H_kv >= 2 ? 576 / H_kv : 512; }
+__host__ __device__ __forceinline__ int kv8_split_len(int n, int H_kv) {
+  const int most = kv8_most_splits(H_kv);
+  const int want = ((n + most - 1) / most + 63) / 64 * 64, least = n <= 4096 ? 256 : 512;
+  return want < least ? least : want > kKv8MaxSplit ? kKv8MaxSplit : want;
 }
-__host__ __device__ __forceinline__ int kv8_n_split(int n) {
-  const int len = kv8_split_len(n);
+__host__ __device__ __forceinline__ int kv8_n_split(int n, int H_kv) {
+  const int len = kv8_split_len(n, H_kv);
   return n <= len ? 1 : static_cast<int>((static_cast<int64_t>(n) + len - 1) / len);
+}
+// the most splits of any row with up to n keys
+inline int kv8_split_bound(int n, int H_kv) {
+  if (n <= 4096) return kv8_n_split(n, H_kv);
+  const int most = kv8_most_splits(H_kv), s = kv8_n_split(n, H_kv);
+  const int low = n <= 512 * most ? 16 : most;
+  return s > low ? s : low;
 }
 
 // A query's weight on a key it does not see is 0, but 0 times the E4M3 NaN is a NaN.  In the steps
