@@ -84,25 +84,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int bt_log = __ffs(c.bt) - 1;
-  int64_t u = blockIdx.x;
-  const int split = static_cast<int>(u % geo.n_split);
-  u /= geo.n_split;
-  const int rt = static_cast<int>(u % geo.row_tiles);
-  u /= geo.row_tiles;
-  const int h = static_cast<int>(u % c.H_kv);
-  const int s = static_cast<int>(u / c.H_kv);
+  // 32-bit divisions: what a CTA does besides its keys counts when a split has 512 of them
+  uint32_t u = blockIdx.x;
+  const int split = static_cast<int>(u % static_cast<uint32_t>(geo.n_split));
+  u /= static_cast<uint32_t>(geo.n_split);
+  const int rt = static_cast<int>(u % static_cast<uint32_t>(geo.row_tiles));
+  u /= static_cast<uint32_t>(geo.row_tiles);
+  const int h = static_cast<int>(u % static_cast<uint32_t>(c.H_kv));
+  const int s = static_cast<int>(u / static_cast<uint32_t>(c.H_kv));
 
   const int q0 = __ldg(a.q_start + s);
   const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
-  const int row0 = rt * kRows;
-  const int64_t all_rows = static_cast<int64_t>(nq) * geo.g;
-  if (nq <= 0 || row0 >= all_rows) return;
-  const int n_row = static_cast<int>(min(static_cast<int64_t>(kRows), all_rows - row0));
+  const uint32_t row0 = rt * kRows, g_heads = geo.g;
+  const uint32_t all_rows = nq > 0 ? nq * g_heads : 0;  // the host keeps max_q * g below 2^31
+  if (row0 >= all_rows) return;
+  const int n_row = static_cast<int>(min(static_cast<uint32_t>(kRows), all_rows - row0));
+  // query of a row of the tile (the first one where there is one, and for the tile's rows past n_row)
+  auto query = [&](int r) -> int { return nq == 1 ? 0 : static_cast<int>((row0 + r) / g_heads); };
   const int p0 = __ldg(a.q_pos0 + s);
   const int kv_all = __ldg(a.kv_len + s);
   const int kv = min(min(kv_all, a.max_kv), c.table_cols * c.bt);
   if (kv < min(kv_all, a.max_kv) && tid == 0) set_status(a.status, LC_DEV_BAD_BLOCK);
-  const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + (row0 + n_row - 1) / geo.g);
+  const int q_first = query(0), q_last = query(n_row - 1);
+  const Kv8Range rg = kv8_range(kv, a.W, p0 + q_first, p0 + q_last);
   const int n = rg.hi - rg.lo16;
   const int len = geo.n_split > 1 ? kv8_split_len(n, c.H_kv) : n;
   const int n_split = geo.n_split > 1 ? kv8_n_split(n, c.H_kv) : 1;
@@ -110,45 +114,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const int k_begin = rg.lo16 + split * len;
   const int k_end = min(rg.hi, k_begin + len);
 
-  // queries: B operand, row g8 of each 8-row tile; the row's power of two goes to the logits
-  uint32_t qf[NT][kKS][2];
-  float f_row[NT][2];  // rows 2 t4, 2 t4 + 1: log2(e) scale 2^eq
-  const int64_t q_stride = a.q_stride ? a.q_stride : static_cast<int64_t>(a.H) * D;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int r = row0 + i * 8 + g8;
-    const bool on = i * 8 + g8 < n_row;
-    uint32_t w[kKS][2];
-    float amax = 0.f;
-    const uint16_t* qr = static_cast<const uint16_t*>(a.q) + (q0 + r / geo.g) * q_stride +
-                         (static_cast<int64_t>(h) * geo.g + r % geo.g) * D;
-#pragma unroll
-    for (int k = 0; k < kKS; ++k) {
-      // dims 16 t + 4 (k % 4) .. + 3, past 64 for the second half
-      uint2 v = make_uint2(0, 0);
-      if (on) v = __ldg(reinterpret_cast<const uint2*>(qr + (k / 4) * 64 + 16 * t4 + 4 * (k % 4)));
-      w[k][0] = v.x;
-      w[k][1] = v.y;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[k][j] << 16)), finite_abs(__uint_as_float(w[k][j] & 0xffff0000u))));
-    }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // largest value into [2^14, 2^15)
-    const int eq = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100) : 0;
-    const float dn = pow2f(-eq);
-#pragma unroll
-    for (int k = 0; k < kKS; ++k)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const __half2 hv = __floats2half2_rn(__uint_as_float(w[k][j] << 16) * dn, __uint_as_float(w[k][j] & 0xffff0000u) * dn);
-        qf[i][k][j] = *reinterpret_cast<const uint32_t*>(&hv);
-      }
-    const float f = a.scale * kLog2e * pow2f(eq);
-    f_row[i][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
-    f_row[i][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
-  }
   // visible keys of this thread's rows
   int r_lo[NT][2], r_hi[NT][2];
 #pragma unroll
@@ -156,13 +121,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int rr = i * 8 + 2 * t4 + j;
-      const Kv8Range x = kv8_range(kv, a.W, p0 + (row0 + rr) / geo.g, p0 + (row0 + rr) / geo.g);
+      const int p = p0 + query(rr);
+      const Kv8Range x = kv8_range(kv, a.W, p, p);
       r_lo[i][j] = x.lo;
       r_hi[i][j] = rr < n_row ? x.hi : 0;
     }
   // keys that every row sees: [all_lo, all_hi)
-  const Kv8Range first = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row0 / geo.g);
-  const Kv8Range last = kv8_range(kv, a.W, p0 + (row0 + n_row - 1) / geo.g, p0 + (row0 + n_row - 1) / geo.g);
+  const Kv8Range first = kv8_range(kv, a.W, p0 + q_first, p0 + q_first);
+  const Kv8Range last = kv8_range(kv, a.W, p0 + q_last, p0 + q_last);
   const int all_lo = last.lo, all_hi = first.hi;
 
   float o[NT][kMT][4];
@@ -177,159 +143,233 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     l[i][0] = l[i][1] = 0.f;
   }
 
+  uint32_t qf[NT][kKS][2];
+  float f_row[NT][2];  // rows 2 t4, 2 t4 + 1: log2(e) scale 2^eq
   bool nan_seen = false;  // NaN value codes replaced in an edge step
-  for (int c0 = k_begin; c0 < k_end; c0 += kChunk) {
-    const int c1 = min(k_end, c0 + kChunk);
-    const int pg0 = c0 >> bt_log;
-    const int n_pg = ((c1 - 1) >> bt_log) - pg0 + 1;
-    if (c0 > k_begin) __syncthreads();
+  int c0 = k_begin, c1 = min(k_end, c0 + kChunk), pg0 = 0, n_pg = 0;
+  auto stage_pages = [&]() {
+    pg0 = c0 >> bt_log;
+    n_pg = ((c1 - 1) >> bt_log) - pg0 + 1;
     for (int i = tid; i < n_pg; i += kThreads) {
       int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + pg0 + i);
       if (blk < 0 || blk >= c.n_blocks) {
         blk = -1;
         set_status(a.status, LC_DEV_BAD_BLOCK);
       }
-      const int64_t slot = static_cast<int64_t>(blk < 0 ? 0 : blk) * c.H_kv + h;
       s_page[i] = blk;
+    }
+  };
+  auto stage_scales = [&]() {
+    for (int i = tid; i < n_pg; i += kThreads) {
+      const int blk = s_page[i];
+      const int64_t slot = static_cast<int64_t>(blk < 0 ? 0 : blk) * c.H_kv + h;
       s_kf[i] = blk < 0 ? 0.f : pow2f(kv8_exp(__ldg(c.k_scale + slot)));
       s_ev[i] = blk < 0 ? 0.f : static_cast<float>(kv8_exp(__ldg(c.v_scale + slot)));
     }
-    __syncthreads();
-
-    Step<D> cur, nxt;
-    auto load = [&](int t0, Step<D>& st) {
-      const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
-      if (pg < 0) return;  // never used
-      const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
-      const uint8_t* kp = c.k + at + g8 * D + 16 * t4;
+  };
+  auto load = [&](int t0, Step<D>& st) {
+    const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
+    if (pg < 0) return;  // never used
+    const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
+    const uint8_t* kp = c.k + at + g8 * D + 16 * t4;
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const uint4 v = ld16(kp + r * 8 * D + x * 64);
-          st.k[r][4 * x] = v.x;
-          st.k[r][4 * x + 1] = v.y;
-          st.k[r][4 * x + 2] = v.z;
-          st.k[r][4 * x + 3] = v.w;
-        }
-      const uint8_t* vp = c.v + at + kVB * g8;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint8_t* p = vp + (2 * t4 + (r & 1) + (r >> 1) * 8) * D;
-        if constexpr (D == 128) {
-          const uint4 v = ld16(p);
-          st.v[r][0] = v.x;
-          st.v[r][1] = v.y;
-          st.v[r][2] = v.z;
-          st.v[r][3] = v.w;
-        } else {
-          const uint2 v = ld8(p);
-          st.v[r][0] = v.x;
-          st.v[r][1] = v.y;
-        }
+      for (int x = 0; x < D / 64; ++x) {
+        const uint4 v = ld16(kp + r * 8 * D + x * 64);
+        st.k[r][4 * x] = v.x;
+        st.k[r][4 * x + 1] = v.y;
+        st.k[r][4 * x + 2] = v.z;
+        st.k[r][4 * x + 3] = v.w;
       }
-    };
+    const uint8_t* vp = c.v + at + kVB * g8;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t* p = vp + (2 * t4 + (r & 1) + (r >> 1) * 8) * D;
+      if constexpr (D == 128) {
+        const uint4 v = ld16(p);
+        st.v[r][0] = v.x;
+        st.v[r][1] = v.y;
+        st.v[r][2] = v.z;
+        st.v[r][3] = v.w;
+      } else {
+        const uint2 v = ld8(p);
+        st.v[r][0] = v.x;
+        st.v[r][1] = v.y;
+      }
+    }
+  };
 
-    load(c0 + warp * 16, cur);
-    for (int t0 = c0 + warp * 16; t0 < c1; t0 += 16 * kWarps) {
-      load(t0 + 16 * kWarps, nxt);
-      const int ip = (t0 >> bt_log) - pg0;
-      if (s_page[ip] >= 0) {
-        const float kf = s_kf[ip], ev = s_ev[ip];
-        const float un_ev = pow2f(-static_cast<int>(ev));
-        const bool edge = t0 < all_lo || t0 + 16 > all_hi;
-        float x[NT][4];
+  auto step = [&](int t0, Step<D>& cur) {
+    const int ip = (t0 >> bt_log) - pg0;
+    if (s_page[ip] >= 0) {
+      const float kf = s_kf[ip], ev = s_ev[ip];
+      const float un_ev = pow2f(-static_cast<int>(ev));
+      const bool edge = t0 < all_lo || t0 + 16 > all_hi;
+      float x[NT][4];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+      for (int i = 0; i < NT; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kKS; ++k) {
-          uint32_t a0, a1, a2, a3;
-          widen4(cur.k[0][k], a0, a2);
-          widen4(cur.k[1][k], a1, a3);
+      for (int k = 0; k < kKS; ++k) {
+        uint32_t a0, a1, a2, a3;
+        widen4(cur.k[0][k], a0, a2);
+        widen4(cur.k[1][k], a1, a3);
 #pragma unroll
-          for (int i = 0; i < NT; ++i) mma16816(x[i], a0, a1, a2, a3, qf[i][k][0], qf[i][k][1]);
-        }
+        for (int i = 0; i < NT; ++i) mma16816(x[i], a0, a1, a2, a3, qf[i][k][0], qf[i][k][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = fmaf(x[i][j], f_row[i][j & 1] * kf, ev);
+      if (edge) {
+        const int ka = t0 + g8, kb = ka + 8;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[i][j] = fmaf(x[i][j], f_row[i][j & 1] * kf, ev);
-        if (edge) {
-          const int ka = t0 + g8, kb = ka + 8;
+          for (int j = 0; j < 2; ++j) {
+            if (ka < r_lo[i][j] || ka >= r_hi[i][j]) x[i][j] = -INFINITY;
+            if (kb < r_lo[i][j] || kb >= r_hi[i][j]) x[i][2 + j] = -INFINITY;
+          }
+        // rows of the block that nobody sees may hold anything: their weight 0 must not meet a NaN
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+        for (int r = 0; r < 4; ++r) {
+          const int key = t0 + 2 * t4 + (r & 1) + (r >> 1) * 8;
+          const bool out = key < rg.lo || key >= rg.hi;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (ka < r_lo[i][j] || ka >= r_hi[i][j]) x[i][j] = -INFINITY;
-              if (kb < r_lo[i][j] || kb >= r_hi[i][j]) x[i][2 + j] = -INFINITY;
-            }
-          // rows of the block that nobody sees may hold anything: their weight 0 must not meet a NaN
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = t0 + 2 * t4 + (r & 1) + (r >> 1) * 8;
-            const bool out = key < rg.lo || key >= rg.hi;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              const uint32_t m = out ? 0xffffffffu : nan_bytes(cur.v[r][q]);
-              nan_seen |= !out && m != 0;
-              cur.v[r][q] &= ~m;
-            }
+          for (int q = 0; q < D / 32; ++q) {
+            const uint32_t m = out ? 0xffffffffu : nan_bytes(cur.v[r][q]);
+            nan_seen |= !out && m != 0;
+            cur.v[r][q] &= ~m;
           }
         }
-        bool up = false;
+      }
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) up |= fmaxf(x[i][j], x[i][2 + j]) > R[i][j] + kHeadroom;
+      if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) up |= fmaxf(x[i][j], x[i][2 + j]) > R[i][j] + kHeadroom;
-        if (__any_sync(0xffffffffu, up)) {
+          for (int j = 0; j < 2; ++j) {
+            float m = fmaxf(x[i][j], x[i][2 + j]);
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            m = fmaxf(m, R[i][j]);
+            const float al = ref_factor(R[i][j], m);
+            R[i][j] = m;
+            l[i][j] *= al;
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float m = fmaxf(x[i][j], x[i][2 + j]);
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              m = fmaxf(m, R[i][j]);
-              const float al = ref_factor(R[i][j], m);
-              R[i][j] = m;
-              l[i][j] *= al;
-#pragma unroll
-              for (int d = 0; d < kMT; ++d) {
-                o[i][d][j] *= al;
-                o[i][d][2 + j] *= al;
-              }
+            for (int d = 0; d < kMT; ++d) {
+              o[i][d][j] *= al;
+              o[i][d][2 + j] *= al;
             }
-        }
-        uint32_t pf[NT][2];
+          }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const float ra = R[i][0] == -INFINITY ? 0.f : R[i][0], rb = R[i][1] == -INFINITY ? 0.f : R[i][1];
+        const float w0 = ex2(x[i][0] - ra), w1 = ex2(x[i][1] - rb), w2 = ex2(x[i][2] - ra), w3 = ex2(x[i][3] - rb);
+        l[i][0] = fmaf(w0 + w2, un_ev, l[i][0]);
+        l[i][1] = fmaf(w1 + w3, un_ev, l[i][1]);
+        const __half2 ha = __floats2half2_rn(w0, w1), hb = __floats2half2_rn(w2, w3);
+        pf[i][0] = movm(*reinterpret_cast<const uint32_t*>(&ha));
+        pf[i][1] = movm(*reinterpret_cast<const uint32_t*>(&hb));
+      }
+#pragma unroll
+      for (int q = 0; q < D / 32; ++q) {
+        // bytes 4q .. 4q + 3 of the thread's dims: tiles 2q, 2q + 1
+        const uint32_t lo0 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x5140), lo1 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x7362);
+        const uint32_t hi0 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x5140), hi1 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x7362);
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        widen4(lo0, a0, a1);
+        widen4(hi0, a2, a3);
+        widen4(lo1, b0, b1);
+        widen4(hi1, b2, b3);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const float ra = R[i][0] == -INFINITY ? 0.f : R[i][0], rb = R[i][1] == -INFINITY ? 0.f : R[i][1];
-          const float w0 = ex2(x[i][0] - ra), w1 = ex2(x[i][1] - rb), w2 = ex2(x[i][2] - ra), w3 = ex2(x[i][3] - rb);
-          l[i][0] = fmaf(w0 + w2, un_ev, l[i][0]);
-          l[i][1] = fmaf(w1 + w3, un_ev, l[i][1]);
-          const __half2 ha = __floats2half2_rn(w0, w1), hb = __floats2half2_rn(w2, w3);
-          pf[i][0] = movm(*reinterpret_cast<const uint32_t*>(&ha));
-          pf[i][1] = movm(*reinterpret_cast<const uint32_t*>(&hb));
-        }
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          // bytes 4q .. 4q + 3 of the thread's dims: tiles 2q, 2q + 1
-          const uint32_t lo0 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x5140), lo1 = __byte_perm(cur.v[0][q], cur.v[1][q], 0x7362);
-          const uint32_t hi0 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x5140), hi1 = __byte_perm(cur.v[2][q], cur.v[3][q], 0x7362);
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          widen4(lo0, a0, a1);
-          widen4(hi0, a2, a3);
-          widen4(lo1, b0, b1);
-          widen4(hi1, b2, b3);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            mma16816(o[i][2 * q], a0, a1, a2, a3, pf[i][0], pf[i][1]);
-            mma16816(o[i][2 * q + 1], b0, b1, b2, b3, pf[i][0], pf[i][1]);
-          }
+          mma16816(o[i][2 * q], a0, a1, a2, a3, pf[i][0], pf[i][1]);
+          mma16816(o[i][2 * q + 1], b0, b1, b2, b3, pf[i][0], pf[i][1]);
         }
       }
-      cur = nxt;
     }
+  };
+
+  // The chain of dependent accesses before the first keys is what a short split waits for: block ids
+  // first, then the first keys, and the queries while those travel
+  Step<D> even, odd;
+  constexpr int kTurn = 16 * kWarps;  // keys that the warps take in one turn
+  if (c0 < c1) stage_pages();
+  __syncthreads();
+  load(c0 + warp * 16, even);
+  if (c0 < c1) stage_scales();
+  // queries: B operand, row g8 of each 8-row tile; the row's power of two goes to the logits
+  const int64_t q_stride = a.q_stride ? a.q_stride : static_cast<int64_t>(a.H) * D;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const bool on = i * 8 + g8 < n_row;
+    const int qi = query(i * 8 + g8);
+    uint32_t w[kKS][2], mb = 0;
+    const uint16_t* qr = static_cast<const uint16_t*>(a.q) + (q0 + qi) * q_stride +
+                         (static_cast<int64_t>(h) * geo.g + (static_cast<int>(row0) + i * 8 + g8 - qi * geo.g)) * D;
+#pragma unroll
+    for (int k = 0; k < kKS; ++k) {
+      // dims 16 t + 4 (k % 4) .. + 3, past 64 for the second half
+      uint2 v = make_uint2(0, 0);
+      if (on) v = __ldg(reinterpret_cast<const uint2*>(qr + (k / 4) * 64 + 16 * t4 + 4 * (k % 4)));
+      w[k][0] = v.x;
+      w[k][1] = v.y;
+      mb = max_u16x2(mb, max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+    }
+    // the largest magnitude as BF16 bits; only where that is not finite the largest finite one
+    mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+    mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+    float amax = __uint_as_float(max(mb & 0xffffu, mb >> 16) << 16);
+    if (__any_sync(0xffffffffu, !(amax < INFINITY))) {
+      amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kKS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[k][j] << 16)), finite_abs(__uint_as_float(w[k][j] & 0xffff0000u))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    }
+    // largest value into [2^14, 2^15)
+    const int eq = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -100) : 0;
+    const float dn = pow2f(-eq);
+#pragma unroll
+    for (int k = 0; k < kKS; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const __half2 hv = __floats2half2_rn(__uint_as_float(w[k][j] << 16) * dn, __uint_as_float(w[k][j] & 0xffff0000u) * dn);
+        qf[i][k][j] = *reinterpret_cast<const uint32_t*>(&hv);
+      }
+    const float f = a.scale * kLog2e * pow2f(eq);
+    f_row[i][0] = __shfl_sync(0xffffffffu, f, 8 * t4);
+    f_row[i][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+  }
+  __syncthreads();
+  while (c0 < c1) {
+    for (int t0 = c0 + warp * 16; t0 < c1; t0 += 2 * kTurn) {
+      load(t0 + kTurn, odd);
+      step(t0, even);
+      if (t0 + kTurn >= c1) break;
+      load(t0 + 2 * kTurn, even);
+      step(t0 + kTurn, odd);
+    }
+    c0 += kChunk;
+    c1 = min(k_end, c0 + kChunk);
+    if (c0 >= c1) break;
+    __syncthreads();  // every warp is done with the block ids
+    stage_pages();
+    __syncthreads();
+    load(c0 + warp * 16, even);
+    stage_scales();
+    __syncthreads();
   }
 
   // join the warps
@@ -364,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       acc.z = fmaf(v.z, f, acc.z);
       acc.w = fmaf(v.w, f, acc.w);
     }
-    const int rr = row0 + r;
+    const int qi = query(r);
     if (nans) {
       // the edge steps that this row sees: below all_lo, and from the step of all_hi on
-      const Kv8Range x = kv8_range(kv, a.W, p0 + rr / geo.g, p0 + rr / geo.g);
+      const Kv8Range x = kv8_range(kv, a.W, p0 + qi, p0 + qi);
       const int lo = max(x.lo, k_begin), hi = min(x.hi, k_end);
       const uint32_t m = kv8_value_nans(c, s, h, lo, min(hi, (all_lo + 15) & ~15), d) |
                          kv8_value_nans(c, s, h, max(lo, all_hi & ~15), hi, d);
@@ -376,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       if (m & 0xff0000u) acc.z = NAN;
       if (m & 0xff000000u) acc.w = NAN;
     }
-    const int head = h * geo.g + rr % geo.g;
-    const int64_t orow = static_cast<int64_t>(q0 + rr / geo.g) * a.H + head;
+    const int head = h * geo.g + (static_cast<int>(row0) + r - qi * geo.g);
+    const int64_t orow = static_cast<int64_t>(q0 + qi) * a.H + head;
     if (n_split > 1) {
       *reinterpret_cast<float4*>(ws_o + (orow * geo.n_split + split) * D + d) = acc;
       if (d == 0) ws_ml[orow * geo.n_split + split] = make_float2(M, L);
@@ -396,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 
 // Joins the splits of each row: a CTA per (query, head), its warps take splits in turn (eight at a
 // time in flight) and meet in shared memory.
-constexpr int kCombineWarps = 8;
+constexpr int kCombineWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo, const float* __restrict__ ws_o,
@@ -407,20 +447,21 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t orow = blockIdx.x;
-  const int q = static_cast<int>(orow / a.H), head = static_cast<int>(orow % a.H);
-  if (q < __ldg(a.q_start) || q >= __ldg(a.q_start + a.num_seqs)) return;
-  const int s = seq_of_query(a.q_start, a.num_seqs, q);
+  const int q = static_cast<int>(blockIdx.x / static_cast<uint32_t>(a.H)), head = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.H));
+  if (!geo.decode && (q < __ldg(a.q_start) || q >= __ldg(a.q_start + a.num_seqs))) return;
+  const int s = geo.decode ? q : seq_of_query(a.q_start, a.num_seqs, q);
   const int q0 = __ldg(a.q_start + s), p0 = __ldg(a.q_pos0 + s);
   const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
   if (q - q0 >= nq) return;
   int n_split = geo.n_split;
   if (!geo.tc) {
     // the range of the row tile that held this row
-    const int rr = (q - q0) * geo.g + head % geo.g;
-    const int row0 = rr / geo.rows * geo.rows;
-    const int row1 = static_cast<int>(min(static_cast<int64_t>(row0) + geo.rows, static_cast<int64_t>(nq) * geo.g)) - 1;
+    const uint32_t rr = (q - q0) * geo.g + static_cast<uint32_t>(head) % static_cast<uint32_t>(geo.g);
+    const uint32_t row0 = rr / static_cast<uint32_t>(geo.rows) * geo.rows;
+    const uint32_t row1 = min(row0 + geo.rows, static_cast<uint32_t>(nq) * geo.g) - 1;
     const int kv = min(min(__ldg(a.kv_len + s), a.max_kv), a.cache.table_cols * a.cache.bt);
-    const Kv8Range rg = kv8_range(kv, a.W, p0 + row0 / geo.g, p0 + row1 / geo.g);
+    const Kv8Range rg = nq == 1 ? kv8_range(kv, a.W, p0, p0)
+                                : kv8_range(kv, a.W, p0 + static_cast<int>(row0 / static_cast<uint32_t>(geo.g)), p0 + static_cast<int>(row1 / static_cast<uint32_t>(geo.g)));
     n_split = kv8_n_split(rg.hi - rg.lo16, a.cache.H_kv);
   }
   if (n_split <= 1) return;
@@ -504,6 +545,7 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
   Kv8Geom geo;
   geo.g = a.H / a.cache.H_kv;
   const int64_t all = static_cast<int64_t>(a.max_q) * geo.g;
+  geo.decode = decode;
   geo.tc = !decode && all >= kTcRows;
   geo.rows = geo.tc ? 256 : geo.g <= 8 ? 8 : 16;
   geo.row_tiles = static_cast<int>((all + geo.rows - 1) / geo.rows);

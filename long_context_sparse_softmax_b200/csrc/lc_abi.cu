@@ -227,6 +227,7 @@ lc_status kv8_attn(const lc_kv8_attn_args* a, void* stream, bool decode) {
     return LC_ERR_ARG;
   if (bad_stride(a->q_stride, static_cast<int64_t>(a->H) * a->cache.D)) return LC_ERR_ARG;
   if (decode && (a->n_q != a->num_seqs || a->max_q > 1)) return LC_ERR_ARG;
+  if (static_cast<int64_t>(a->max_q) * a->H > INT32_MAX || static_cast<int64_t>(a->n_q) * a->H > INT32_MAX) return LC_ERR_ARG;  // rows
   if (a->n_q == 0 || a->num_seqs == 0 || a->max_q == 0) return LC_OK;
   LC_TRY(check_kv8(a->cache, a->max_kv > 0));
   if (!a->q || !a->q_start || !a->q_pos0 || !a->kv_len || !a->out) return LC_ERR_ARG;

@@ -39,14 +39,15 @@ __device__ __forceinline__ Kv8Range kv8_range(int kv, int W, int p_first, int p_
 
 // Split of n keys over CTAs: `len` keys each.  A function of the row's own key count and of the
 // shared heads alone, so a sequence's result does not depend on the batch it is in.  256 keys where
-// a sequence is short and its latency counts, 512 above 4096 keys (a split costs 8 partial rows of
-// D FP32 values next to 2 D bytes a key: 3 %), and from most_splits * 512 keys on as many as fill
-// the device with one sequence (576 CTAs: 4 on each multiprocessor), up to 8192 keys each.
+// a sequence is short and its latency counts, 512 above 4096 keys, 1024 above 8192 (what a CTA does
+// besides its keys, and the partial rows, cost as much as 200 keys), and from most_splits * 1024
+// keys on as many as fill the device with one sequence (576 CTAs: 4 on each multiprocessor), up to
+// 8192 keys each.
 constexpr int kKv8MaxSplit = 8192;
 __host__ __device__ __forceinline__ int kv8_most_splits(int H_kv) { return H_kv >= 8 ? 72 : H_kv >= 2 ? 576 / H_kv : 512; }
 __host__ __device__ __forceinline__ int kv8_split_len(int n, int H_kv) {
   const int most = kv8_most_splits(H_kv);
-  const int want = ((n + most - 1) / most + 63) / 64 * 64, least = n <= 4096 ? 256 : 512;
+  const int want = ((n + most - 1) / most + 63) / 64 * 64, least = n <= 4096 ? 256 : n <= 8192 ? 512 : 1024;
   return want < least ? least : want > kKv8MaxSplit ? kKv8MaxSplit : want;
 }
 __host__ __device__ __forceinline__ int kv8_n_split(int n, int H_kv) {
@@ -57,7 +58,7 @@ __host__ __device__ __forceinline__ int kv8_n_split(int n, int H_kv) {
 inline int kv8_split_bound(int n, int H_kv) {
   if (n <= 4096) return kv8_n_split(n, H_kv);
   const int most = kv8_most_splits(H_kv), s = kv8_n_split(n, H_kv);
-  const int low = n <= 512 * most ? 16 : most;
+  const int low = n <= 1024 * most ? 16 : most;  // 16: at 4096 and at 8192 keys
   return s > low ? s : low;
 }
 
@@ -96,6 +97,7 @@ struct Kv8Geom {
   int n_split;    // CTAs per row tile (1: no split); of k_kv8_attn an upper bound
   int rows;       // rows per row tile
   int tc;         // k_kv8_attn_tc: every row has n_split partial results
+  int decode;     // query s belongs to sequence s
 };
 
 cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,

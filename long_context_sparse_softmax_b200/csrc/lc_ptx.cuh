@@ -202,6 +202,12 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 // ---------------------------------------------------------------- arithmetic
+// the larger of each pair of 16-bit numbers
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // pairs of FP32 values (one instruction for two products or sums)
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
