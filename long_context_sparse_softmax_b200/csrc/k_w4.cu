@@ -32,10 +32,11 @@ constexpr int kK = 128;                 // inputs per step
 constexpr int kTileA = kM * kK;         // bytes of A in shared memory (padded codes)
 constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 rows of 4 words
 // warps by role
-constexpr int kTurns = 2;               // warps of a role that take steps in turn: divides kStages, so that a stage
-                                        // always has the same ones and no barrier is waited for a round too early
-constexpr int kXT = 256;                // threads of a turn that turn x into B's columns
-constexpr int kWarpX = 4 * kTurns, kWarpLw = kWarpX + kXT / 32 * kTurns, kWarpLx = kWarpLw + 2, kWarpMma = kWarpLx + 2;
+// Warps of a role take steps in turn.  The turns divide kStages, so that a stage always has the same
+// ones and no barrier is waited for a round too early (and are at most kRawW, kRawX, likewise).
+constexpr int kTurns = 2, kTurnsX = 4;
+constexpr int kXT = 128;                // threads of a turn that turn x into B's columns
+constexpr int kWarpX = 4 * kTurns, kWarpLw = kWarpX + kXT / 32 * kTurnsX, kWarpLx = kWarpLw + 2, kWarpMma = kWarpLx + 2;
 constexpr int kThreads = 32 * (kWarpMma + kTurns);
 constexpr long kSpin = 1L << 20;  // a few seconds
 
@@ -46,14 +47,16 @@ struct W4Smem {
   static constexpr int kTok = kMx ? N : N / 2;
   static constexpr int kUnits = kTok * (kMx ? 8 : 16);    // 16-byte units of x per step
   static constexpr int kStages = 4;
-  static constexpr int kRawX = 6;
-  static constexpr int kRawW = 8;
+  static constexpr int kRawX = N <= 32 ? 6 : 4;
+  static constexpr int kRawW = N <= 32 ? 8 : 6;
   static constexpr int kStage = kTileA + N * kK + 2 * kSf;
   static constexpr int kRawWBytes = kM * kK / 2 + kM * 4;
   static constexpr int kRawXBytes = kUnits * 16 + (kMx ? kTok * 4 : 0);
   static constexpr int kRing = kStages * kStage, kW = kRawW * kRawWBytes, kX = kRawX * kRawXBytes;
-  static constexpr int kBytes = kRing + kW + kX + 1024;
-  static_assert(kStages % kTurns == 0 && kTok * kM * 4 <= kW, "turns, partial sums");
+  // a CTA's share of the joined rows: (n_tok + split - 1) / split rows of `split` partial sums
+  static constexpr int kPart = (kTok + 7) * kM * 4;
+  static constexpr int kBytes = kRing + kW + kX + kPart + 1024;
+  static_assert(kStages % kTurns == 0 && kStages % kTurnsX == 0 && kRawX >= kTurnsX && kRawW >= kTurns, "turns");
 };
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
@@ -112,12 +115,10 @@ __device__ __forceinline__ uint16_t f16x2_to_e4m3x2(__half2 v) {
 }
 __device__ __forceinline__ __half2 e4m3x2_to_f16x2(uint16_t v) { return __half2(__nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3)); }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t rank, float v) {
   uint32_t r;
-  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(r) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(r), "f"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
@@ -139,7 +140,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   uint8_t* SFb = SFa + kStages * kSf;              // [kStages][kSf]
   uint8_t* Xr = SFb + kStages * kSf;               // [kRawX][kRawXBytes]
   uint8_t* Wr = Xr + L::kX;                        // [kRawW][kRawWBytes]
-  float* part = reinterpret_cast<float*>(Wr);      // after the last step: the partial tile of a cluster's CTA [kTok][kM]
+  // partial sums of a cluster: the row's place in the share of the CTA that adds it up, rank, output
+  float* part = reinterpret_cast<float*>(Wr + L::kW);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
@@ -194,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   __syncthreads();
   fence_after();
   const uint32_t tm = s_tmem;
+  if (split > 1) cluster_arrive();  // this CTA runs: its peers can write to its shared memory (they wait below)
 
   // The copying warps never meet a proxy fence: it would wait for every copy still in flight (1000 cycles
   // a step).  The converting warps, which need one before the tensor core reads, copy nothing.
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
     const bool scaler = xc % (kLpr / 4) == 0;
     const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + L::kUnits * 16 + t0 * 4;
 #pragma unroll 1
-    for (int i = (warp - kWarpX) / (kXT / 32); i < n_step; i += kTurns) {
+    for (int i = (warp - kWarpX) / (kXT / 32); i < n_step; i += kTurnsX) {
       const int st = i % kStages, slot = i % L::kRawX;
       if (!wait(&xfull[slot], (i / L::kRawX) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
       const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
@@ -425,25 +428,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   }
   __syncwarp();
 
-  // ---------------- epilogue: thread r of warps 0-3 holds output c0 + r for every column
-  const bool ok = warp < 4 ? __all_sync(0xffffffffu, wait(&done, 0)) : true;
-  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  // ---------------- epilogue: warps 0 .. 27, four take 8 rows of x at a time; lane r of their 128 holds
+  // output c0 + r
+  const bool ok = __all_sync(0xffffffffu, wait(&done, 0));
   auto store = [&](int t, int r, float v) {
     const int64_t at = static_cast<int64_t>(n0 + t) * a.G * a.d_g + static_cast<int64_t>(g) * a.d_g + c0 + r;
     if (a.out_fmt == LC_FMT_F32) static_cast<float*>(a.y)[at] = v;
     else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_bits(v);
   };
-  if (warp < 4) {
-    fence_after();
+  if (split > 1) cluster_wait();
+  fence_after();
+  if (warp < kWarpMma) {
+    const int r = (warp & 3) * 32 + lane;
 #pragma unroll 1
-    for (int t0 = 0; t0 < n_tok; t0 += 8) {
+    for (int t0 = (warp >> 2) * 8; t0 < n_tok; t0 += 8 * (kWarpMma / 4)) {
       // an issuing warp that had no step left its sums unwritten
       constexpr int kSum = kMx ? kTurns : 2 * kTurns;
       uint32_t v[kSum][8];
 #pragma unroll
       for (int q = 0; q < kSum; ++q)
-        tmem_ld8(tm + lane_off + (kMx ? q : q / 2) * kAcc + (kMx ? 0 : (q & 1) * kTok) + t0, v[q]);
+        tmem_ld8(tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (kMx ? q : q / 2) * kAcc + (kMx ? 0 : (q & 1) * kTok) + t0, v[q]);
       tmem_wait_ld();
+      int own = t0 % split, place = t0 / split * split + rank;  // of row t: the CTA that adds it up, the place there
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int t = t0 + j;
@@ -451,9 +457,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
 #pragma unroll
         for (int q = 1; q < kSum; ++q)
           if ((kMx ? q : q / 2) < n_step) y += __uint_as_float(v[q][j]);
+        if (t >= n_tok || !ok) break;
         if (split > 1) {
-          if (t < n_tok) part[t * kM + tid] = y;
-        } else if (ok && t < n_tok && tid < rows) store(t, tid, y);
+          st_cluster_f32(su32(part + place * kM + r), own, y);
+          if (++own == split) {
+            own = 0;
+            place += split;
+          }
+        } else if (r < rows) {
+          store(t, r, y);
+        }
       }
     }
   }
@@ -461,26 +474,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(tm, kCols);
   if (split > 1) {
+    __syncwarp();
     cluster_arrive();
-    cluster_wait();  // every partial tile is in place
-    // this CTA's share of the rows of x (t % split == rank), 4 outputs a thread, added in the order of ranks
-    const int items = (n_tok - rank + split - 1) / split * (kM / 4);
+    cluster_wait();  // every partial sum is in place
+    // this CTA's share of the rows of x (t % split == rank), added in the order of ranks
+    const int items = (n_tok - rank + split - 1) / split * kM;
     for (int u = tid; u < items; u += kThreads) {
-      const int t = u / (kM / 4) * split + rank, r = u % (kM / 4) * 4;
-      const uint32_t at = su32(part + t * kM + r);
-      float4 y = ld_cluster_f32x4(at, 0);
-#pragma unroll 4
-      for (int p = 1; p < split; ++p) {
-        const float4 v = ld_cluster_f32x4(at, p);
-        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-      }
-      if (r < rows) store(t, r, y.x);
-      if (r + 1 < rows) store(t, r + 1, y.y);
-      if (r + 2 < rows) store(t, r + 2, y.z);
-      if (r + 3 < rows) store(t, r + 3, y.w);
+      const int q = u / kM, r = u % kM;
+      const float* p = part + q * split * kM + r;
+      float y = p[0];
+      for (int k = 1; k < split; ++k) y += p[k * kM];
+      if (ok && r < rows) store(q * split + rank, r, y);
     }
-    cluster_arrive();
-    cluster_wait();  // and read by the peers before it goes
   }
 }
 
