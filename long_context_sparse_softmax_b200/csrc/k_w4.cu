@@ -19,6 +19,8 @@
 // multiprocessors; the partial tiles meet in distributed shared memory and are added in rank
 // order, so the result does not depend on timing.  Every mbarrier wait is bounded
 // (LC_DEV_TIMEOUT).
+#include <cuda.h>
+
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
 #include "lc_ptx.cuh"
@@ -36,7 +38,7 @@ constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 ro
 // ones and no barrier is waited for a round too early (and are at most kRawW, kRawX, likewise).
 constexpr int kTurns = 2, kTurnsX = 4;
 constexpr int kXT = 128;                // threads of a turn that turn x into B's columns
-constexpr int kWarpX = 4 * kTurns, kWarpLw = kWarpX + kXT / 32 * kTurnsX, kWarpLx = kWarpLw + 2, kWarpMma = kWarpLx + 2;
+constexpr int kWarpX = 4 * kTurns, kWarpCopy = kWarpX + kXT / 32 * kTurnsX, kWarpMma = kWarpCopy + 2;
 constexpr int kThreads = 32 * (kWarpMma + kTurns);
 constexpr long kSpin = 1L << 20;  // a few seconds
 
@@ -48,27 +50,16 @@ struct W4Smem {
   static constexpr int kUnits = kTok * (kMx ? 8 : 16);    // 16-byte units of x per step
   static constexpr int kStages = 4;
   static constexpr int kRawX = N <= 32 ? 6 : 4;
-  static constexpr int kRawW = N <= 32 ? 8 : 6;
+  static constexpr int kRawW = N <= 32 ? 5 : 3;           // of two steps each: a row's 128 bytes
   static constexpr int kStage = kTileA + N * kK + 2 * kSf;
-  static constexpr int kRawWBytes = kM * kK / 2 + kM * 4;
-  static constexpr int kRawXBytes = kUnits * 16 + (kMx ? kTok * 4 : 0);
+  static constexpr int kRawWBytes = kM * kK, kRawXBytes = kUnits * 16;
   static constexpr int kRing = kStages * kStage, kW = kRawW * kRawWBytes, kX = kRawX * kRawXBytes;
   // a CTA's share of the joined rows: (n_tok + split - 1) / split rows of `split` partial sums
   static constexpr int kPart = (kTok + 7) * kM * 4;
   static constexpr int kBytes = kRing + kW + kX + kPart + 1024;
-  static_assert(kStages % kTurns == 0 && kStages % kTurnsX == 0 && kRawX >= kTurnsX && kRawW >= kTurns, "turns");
+  static_assert(kStages % kTurns == 0 && kStages % kTurnsX == 0 && kRawX >= kTurnsX && kTurns == 2, "turns");
 };
 
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
-}
-// this thread's copies so far arrive on `bar` once complete
-__device__ __forceinline__ void cp_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
-}
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -127,7 +118,8 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // N: columns of B (a multiple of 16: 2 per BF16 row, 1 per MXFP8 row)
 template <int N, bool kMx>
-__global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int split, int tiles_g) {
+__global__ void __launch_bounds__(kThreads, 1)
+    k_w4_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, lc_w4_proj_args a, int split, int tiles_g) {
   using L = W4Smem<N, kMx>;
   constexpr int kStages = L::kStages, kTok = L::kTok;
   constexpr int kAcc = N + 16;                    // tensor-memory columns of an issuing warp: sums, scales
@@ -138,10 +130,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   uint8_t* Bs = As + kStages * kTileA;             // [kStages][N * kK]
   uint8_t* SFa = Bs + kStages * N * kK;            // [kStages][kSf]
   uint8_t* SFb = SFa + kStages * kSf;              // [kStages][kSf]
-  uint8_t* Xr = SFb + kStages * kSf;               // [kRawX][kRawXBytes]
-  uint8_t* Wr = Xr + L::kX;                        // [kRawW][kRawWBytes]
+  uint8_t* Wr = SFb + kStages * kSf;               // [kRawW][kRawWBytes], in multiples of 1024 bytes so far
+  uint8_t* Xr = Wr + L::kW;                        // [kRawX][kRawXBytes]
   // partial sums of a cluster: the row's place in the share of the CTA that adds it up, rank, output
-  float* part = reinterpret_cast<float*>(Wr + L::kW);
+  float* part = reinterpret_cast<float*>(Xr + L::kX);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
@@ -155,8 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   const int n0 = static_cast<int>(blockIdx.y) * kTok;      // first row of x
   const int n_tok = min(kTok, a.n_q - n0);
   const int n_sub = (a.K + kK - 1) / kK;
-  const int s_begin = static_cast<int>(static_cast<int64_t>(n_sub) * rank / split);
-  const int n_step = static_cast<int>(static_cast<int64_t>(n_sub) * (rank + 1) / split) - s_begin;
+  // this rank's steps: whole pairs (a pair of steps is 128 bytes of a row of codes)
+  const int n_pair = (n_sub + 1) / 2;
+  const int s_begin = 2 * static_cast<int>(static_cast<int64_t>(n_pair) * rank / split);
+  const int n_step = min(n_sub, 2 * static_cast<int>(static_cast<int64_t>(n_pair) * (rank + 1) / split)) - s_begin;
   const int rows = min(kM, a.d_g - c0);
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -178,15 +172,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
       mbar_init(su32(&empty[i]), 1);
     }
     for (int i = 0; i < L::kRawW; ++i) {
-      mbar_init(su32(&wfull[i]), 64);
-      mbar_init(su32(&wempty[i]), 128);
+      mbar_init(su32(&wfull[i]), 1);
+      mbar_init(su32(&wempty[i]), 256);
     }
     for (int i = 0; i < L::kRawX; ++i) {
-      mbar_init(su32(&xfull[i]), 64);
+      mbar_init(su32(&xfull[i]), 1);
       mbar_init(su32(&xempty[i]), kXT);
     }
     mbar_init(su32(&done), kTurns);
     fence_mbar_init();
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_x);
   }
   // columns of B without a row of x stay zero (scale 2^0) in every stage
   for (int i = tid; i < kStages * N * kK / 16; i += kThreads) reinterpret_cast<uint4*>(Bs)[i] = make_uint4(0, 0, 0, 0);
@@ -198,148 +194,103 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   const uint32_t tm = s_tmem;
   if (split > 1) cluster_arrive();  // this CTA runs: its peers can write to its shared memory (they wait below)
 
-  // The copying warps never meet a proxy fence: it would wait for every copy still in flight (1000 cycles
-  // a step).  The converting warps, which need one before the tensor core reads, copy nothing.
   const bool words = a.K % 128 == 0;  // a row's four scale bytes of a step are one aligned word
-  auto copies_arrive = [&](uint32_t bar) {
-    if (words) {
-      cp_arrive(bar);
-    } else {  // scale words were stored, too
-      asm volatile("cp.async.wait_all;\n" ::: "memory");
-      mbar_arrive(bar);
+  if (warp == kWarpCopy || warp == kWarpCopy + 1) {
+    // ---------------- copies: one thread for the codes, one for x.  Rows of 128 bytes: with 64 (a step at
+    // a time) the copies of a step took 650 cycles, whoever made them
+    if (lane == 0) {
+      const bool codes = warp == kWarpCopy;
+      const int n = codes ? (n_step + 1) / 2 : n_step, ring = codes ? L::kRawW : L::kRawX;
+      uint64_t *full_b = codes ? wfull : xfull, *empty_b = codes ? wempty : xempty;
+      const uint32_t dst = su32(codes ? Wr : Xr), bytes = codes ? L::kRawWBytes : L::kRawXBytes;
+      const CUtensorMap* map = codes ? &map_w : &map_x;
+      const int row = codes ? g * a.d_g + c0 : n0, step = codes ? kK : kK * (kMx ? 1 : 2);
+      int col = codes ? s_begin * (kK / 2) : (g * a.K + s_begin * kK) * (kMx ? 1 : 2);
+      int i = 0;
+      for (; i < n; ++i, col += step) {
+        const int slot = i % ring;
+        if (i >= ring && !wait(&empty_b[slot], ((i / ring) - 1) & 1)) break;
+        mbar_expect_tx(su32(&full_b[slot]), bytes);
+        tma_tile2d(dst + slot * bytes, map, col, row, su32(&full_b[slot]));
+      }
+      // a role that gave up leaves copies in flight: they land (in bounded time) before the CTA ends
+      if (i < n)
+        for (int q = max(0, i - ring); q < i; ++q)
+          for (long it = 0; it < kSpin && !mbar_test(su32(&full_b[q % ring]), (q / ring) & 1); ++it) {
+          }
     }
-  };
-  if (warp >= kWarpLw && warp < kWarpLx) {
-    // ---------------- copies of the weights: 16 bytes (32 codes) of 8 rows a thread and step
-    const int64_t row_g = static_cast<int64_t>(g) * a.d_g + c0;
-    const int lt = tid & 63, seg = lt & 3, r0 = lt >> 2;  // rows r0 + 16 j
-    const uint8_t* wp = a.w + (row_g + r0) * (a.K / 2) + static_cast<int64_t>(s_begin) * (kK / 2) + seg * 16;
-    const int64_t r16 = static_cast<int64_t>(a.K) * 8;       // 16 rows further
-    const uint8_t* sp = a.w_scale + (row_g + lt) * (a.K / 32) + s_begin * 4;
-    const uint32_t raw = su32(Wr) + lt * 16, raws = su32(Wr) + kM * kK / 2 + lt * 4;
-    int slot = 0, round = 0;
-#pragma unroll 1
-    for (int i = 0; i < n_step; ++i) {
-      if (round > 0 && !wait(&wempty[slot], (round - 1) & 1)) break;
-      const bool k_in = (s_begin + i) * kK + seg * 32 < a.K;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool v = k_in && r0 + 16 * j < rows;
-        cp_async16z(raw + slot * L::kRawWBytes + j * 1024, v ? wp + j * r16 : a.w, v);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (lt + 64 * h >= rows) continue;
-        const uint8_t* p = sp + h * 64 * static_cast<int64_t>(a.K / 32);
-        if (words) {
-          cp_async4(raws + slot * L::kRawWBytes + h * 256, p);
-        } else {
-          uint32_t sw = 0x7f7f7f7fu;
-          const int nb = a.K / 32 - (s_begin + i) * 4;  // scale bytes left in the row
-          for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(p + b)) << (8 * b);
-          st_shared4(raws + slot * L::kRawWBytes + h * 256, sw);
-        }
-      }
-      copies_arrive(su32(&wfull[slot]));
-      wp += kK / 2;
-      sp += 4;
-      if (++slot == L::kRawW) {
-        slot = 0;
-        ++round;
-      }
-    }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
   } else if (warp < kWarpX) {
     // ---------------- the weights into A's layout (8-byte copies would land there by themselves, but ran
     // at a third of the rate): codes 32 seg .. + 15 and + 16 .. + 31 of a row are the first 8 bytes of
     // slots 2 seg and 2 seg + 1
-    const int wt = tid & 127, seg = wt & 3, r0 = wt >> 2;
-    const uint32_t raw = su32(Wr) + wt * 16, raws = su32(Wr) + kM * kK / 2 + wt * 4;
+    // lanes take rows 4 apart in pairs: in the 128-byte swizzle their pieces fall into different banks
+    const int wt = tid & 127, seg = wt & 3, r0 = (wt & ~31) / 4 + (lane >> 3) + (lane & 4);
+    const uint32_t raw = su32(Wr) + sw128_off(r0, (warp >> 2) * 4 + seg);  // turn 0 has the first half of each pair
     const uint32_t d0 = su32(As) + sw128_off(r0, 2 * seg), d1 = su32(As) + sw128_off(r0, 2 * seg + 1);
     const uint32_t ds = su32(SFa) + sf_off(wt, 0);
+    // the row's scales of a step, a turn ahead
+    const uint8_t* sp = a.w_scale + (static_cast<int64_t>(g) * a.d_g + c0 + wt) * (a.K / 32) + s_begin * 4;
+    auto scale_word = [&](int i) -> uint32_t {
+      if (wt >= rows || i >= n_step) return 0x7f7f7f7fu;
+      if (words) return __ldg(reinterpret_cast<const uint32_t*>(sp + i * 4));
+      uint32_t w = 0x7f7f7f7fu;
+      const int nb = a.K / 32 - (s_begin + i) * 4;  // scale bytes left in the row
+      for (int b = 0; b < min(nb, 4); ++b) w ^= (0x7fu ^ __ldg(sp + i * 4 + b)) << (8 * b);
+      return w;
+    };
+    uint32_t sw = scale_word(warp >> 2);
 #pragma unroll 1
     for (int i = warp >> 2; i < n_step; i += kTurns) {
-      const int st = i % kStages, slot = i % L::kRawW;
-      if (!wait(&wfull[slot], (i / L::kRawW) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
+      const int st = i % kStages, slot = i / 2 % L::kRawW;
+      if (!wait(&wfull[slot], (i / 2 / L::kRawW) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 v = ld_shared16(raw + slot * L::kRawWBytes + j * 2048);
+        const uint4 v = ld_shared16(raw + slot * L::kRawWBytes + j * 4096);
         st_shared8(d0 + st * kTileA + j * 4096, v.x, v.y);
         st_shared8(d1 + st * kTileA + j * 4096, v.z, v.w);
       }
-      st_shared4(ds + st * kSf, wt < rows ? ld_shared4(raws + slot * L::kRawWBytes) : 0x7f7f7f7fu);
+      st_shared4(ds + st * kSf, sw);
+      sw = scale_word(i + kTurns);
       mbar_arrive(su32(&wempty[slot]));
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
     }
-  } else if (warp >= kWarpLx && warp < kWarpMma) {
-    // ---------------- copies of x: 16 bytes a lane
-    constexpr int kLpr = kMx ? 8 : 16, kXTok = 64 / kLpr;  // lanes per row, rows at once
-    constexpr int kB = kMx ? 1 : 2;
-    const int xt = tid & 63, xc = xt % kLpr, t0 = xt / kLpr;
-    const int64_t ldx = static_cast<int64_t>(a.G) * a.K;
-    const int64_t at = (n0 + t0) * ldx + static_cast<int64_t>(g) * a.K + static_cast<int64_t>(s_begin) * kK + xc * (kK / kLpr);
-    const uint8_t* xp = static_cast<const uint8_t*>(a.x) + at * kB;   // of the step
-    const uint8_t* sp = kMx ? a.x_scale + at / 32 : nullptr;
-    const int64_t row_x = kXTok * ldx * kB, row_s = kXTok * ldx / 32;
-    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + L::kUnits * 16 + t0 * 4;
-    const int n_it = (n_tok + kXTok - 1) / kXTok;
-    int slot = 0, round = 0;
-#pragma unroll 1
-    for (int i = 0; i < n_step; ++i) {
-      if (round > 0 && !wait(&xempty[slot], (round - 1) & 1)) break;
-      const int nb = a.K / 32 - (s_begin + i) * 4;  // blocks left in the row
-      const bool in = xc / (kLpr / 4) < nb;
-      const uint32_t dst = raw + slot * L::kRawXBytes, dsts = raws + slot * L::kRawXBytes;
-      const uint8_t *p = xp, *q = sp;
-      int t = t0;
-#pragma unroll 2
-      for (int m = 0; m < n_it; ++m) {
-        const bool v = in && t < n_tok;
-        cp_async16z(dst + m * 1024, v ? p : static_cast<const uint8_t*>(a.x), v);
-        if (kMx && xc == 0 && t < n_tok) {
-          if (words) {
-            cp_async4(dsts + m * kXTok * 4, q);
-          } else {
-            uint32_t sw = 0x7f7f7f7fu;
-            for (int b = 0; b < min(nb, 4); ++b) sw ^= (0x7fu ^ __ldg(q + b)) << (8 * b);
-            st_shared4(dsts + m * kXTok * 4, sw);
-          }
-        }
-        p += row_x;
-        q += row_s;
-        t += kXTok;
-      }
-      copies_arrive(su32(&xfull[slot]));
-      xp += kK * kB;
-      sp += 4;
-      if (++slot == L::kRawX) {
-        slot = 0;
-        ++round;
-      }
-    }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
-  } else if (warp < kWarpLw) {
+  } else if (warp < kWarpCopy) {
     // ---------------- x into B's columns.  Four lanes share a 32-value block of a BF16 row (8 values each),
     // two a block of MXFP8 codes
     constexpr int kLpr = kMx ? 8 : 16, kXTok = kXT / kLpr;
     const int xt = (tid - 32 * kWarpX) % kXT, xc = xt % kLpr, xb = xc / (kLpr / 4), t0 = xt / kLpr;
     const bool scaler = xc % (kLpr / 4) == 0;
-    const uint32_t raw = su32(Xr) + xt * 16, raws = su32(Xr) + L::kUnits * 16 + t0 * 4;
+    const uint32_t raw = su32(Xr) + xt * 16;
+    constexpr int kU = (kTok + kXTok - 1) / kXTok;
+    // MXFP8: a block's scale byte, a turn ahead
+    const int64_t ld_s = static_cast<int64_t>(a.G) * (a.K / 32);
+    const uint8_t* sp = kMx ? a.x_scale + (n0 + t0) * ld_s + static_cast<int64_t>(g) * (a.K / 32) + s_begin * 4 + xb : nullptr;
+    uint8_t sc[kU];
+    auto scale_bytes = [&](int i) {
+      const bool in = i < n_step && scaler && (s_begin + i) * 4 + xb < a.K / 32;
+#pragma unroll
+      for (int m = 0; m < kU; ++m)
+        sc[m] = in && t0 + kXTok * m < n_tok ? __ldg(sp + i * 4 + m * kXTok * ld_s) : static_cast<uint8_t>(127);
+    };
+    const int first = (warp - kWarpX) / (kXT / 32);
+    if constexpr (kMx) scale_bytes(first);
 #pragma unroll 1
-    for (int i = (warp - kWarpX) / (kXT / 32); i < n_step; i += kTurnsX) {
+    for (int i = first; i < n_step; i += kTurnsX) {
       const int st = i % kStages, slot = i % L::kRawX;
       if (!wait(&xfull[slot], (i / L::kRawX) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
       const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
-#pragma unroll 2
-      for (int m = 0; m < (kTok + kXTok - 1) / kXTok; ++m) {
+      const bool in = (s_begin + i) * 4 + xb < a.K / 32;  // else the next group's values
+#pragma unroll
+      for (int m = 0; m < kU; ++m) {
         const int t = t0 + kXTok * m;
         if (t - (lane / kLpr) >= n_tok) break;  // the same for every lane
-        const uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * (kXT * 16));
+        uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * (kXT * 16));
+        if (!in) v = make_uint4(0, 0, 0, 0);
         if constexpr (kMx) {
           if (t >= n_tok) continue;
           st_shared16(Bt + sw128_off(t, xc), v);
-          if (scaler) st_shared1(sf + sf_off(t, xb), ld_shared4(raws + slot * L::kRawXBytes + m * kXTok * 4) >> (8 * xb));
+          if (scaler) st_shared1(sf + sf_off(t, xb), sc[m]);
         } else {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           // the block's largest magnitude as BF16 bits (an infinity's or a NaN's are larger still)
@@ -382,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
         }
       }
       mbar_arrive(su32(&xempty[slot]));
+      if constexpr (kMx) scale_bytes(i + kTurnsX);
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
     }
@@ -428,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   }
   __syncwarp();
 
-  // ---------------- epilogue: warps 0 .. 27, four take 8 rows of x at a time; lane r of their 128 holds
+  // ---------------- epilogue: warps 0 .. 23, four take 8 rows of x at a time; lane r of their 128 holds
   // output c0 + r
   const bool ok = __all_sync(0xffffffffu, wait(&done, 0));
   auto store = [&](int t, int r, float v) {
@@ -438,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
   };
   if (split > 1) cluster_wait();
   fence_after();
-  if (warp < kWarpMma) {
+  if (warp < kWarpCopy) {
     const int r = (warp & 3) * 32 + lane;
 #pragma unroll 1
-    for (int t0 = (warp >> 2) * 8; t0 < n_tok; t0 += 8 * (kWarpMma / 4)) {
+    for (int t0 = (warp >> 2) * 8; t0 < n_tok; t0 += 8 * (kWarpCopy / 4)) {
       // an issuing warp that had no step left its sums unwritten
       constexpr int kSum = kMx ? kTurns : 2 * kTurns;
       uint32_t v[kSum][8];
@@ -491,15 +443,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_proj(lc_w4_proj_args a, int 
 
 namespace {
 
+using EncodeBytes = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeBytes encode_bytes() {
+  static EncodeBytes fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeBytes>(nullptr);
+    return reinterpret_cast<EncodeBytes>(f);
+  }();
+  return fn;
+}
+
+// [rows, cols] bytes, row-major, box_cols x box_rows boxes as they lie; what is past either end reads as 0.
+// cols and box_cols are multiples of 16, and so is every column that a copy starts at
+bool byte_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t es[2] = {1, 1};
+  return encode_bytes()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int N, bool kMx>
 cudaError_t launch_w4(const lc_w4_proj_args& a, int split, int tiles_g, cudaStream_t st) {
   constexpr int kTok = kMx ? N : N / 2;
   constexpr size_t smem = W4Smem<N, kMx>::kBytes;
   static_assert(smem <= 227 * 1024 - 512, "shared memory");
+  CUtensorMap map_w, map_x;
+  if (!encode_bytes()) return cudaErrorNotSupported;
+  if (!byte_map(&map_w, a.w, static_cast<int64_t>(a.G) * a.d_g, a.K / 2, kK, kM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !byte_map(&map_x, a.x, a.n_q, static_cast<int64_t>(a.G) * a.K * (kMx ? 1 : 2), kK * (kMx ? 1 : 2), kTok, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(a.G * tiles_g * split), static_cast<unsigned>((a.n_q + kTok - 1) / kTok));
   const cudaError_t e = cudaFuncSetAttribute(k_w4_proj<N, kMx>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const cudaError_t r = launch_ex(k_w4_proj<N, kMx>, grid, dim3(kThreads), smem, st, false, split, a, split, tiles_g);
+  const cudaError_t r = launch_ex(k_w4_proj<N, kMx>, grid, dim3(kThreads), smem, st, false, split, map_w, map_x, a, split, tiles_g);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 

@@ -180,7 +180,7 @@ lc_status w4_proj(const lc_w4_proj_args* a, void* stream) {
   if (!mx && a->in_fmt != LC_FMT_BF16) return LC_ERR_ARG;
   // launch limits: 2^31 - 1 CTAs in x, 65535 in y
   const int64_t tiles = static_cast<int64_t>(a->G) * ((static_cast<int64_t>(a->d_g) + 127) / 128);
-  if (tiles > (int64_t{1} << 27) || static_cast<int64_t>(a->G) * a->K > (int64_t{1} << 30) ||
+  if (tiles > (int64_t{1} << 24) || static_cast<int64_t>(a->G) * a->K > (int64_t{1} << 30) ||
       (static_cast<int64_t>(a->n_q) + 63) / 64 > 65535)
     return LC_ERR_UNSUPPORTED;
   if (a->n_q == 0) return LC_OK;
