@@ -10,15 +10,25 @@
 // fits the other 4: hi + lo is x exactly down to 2^-15 of the block's largest value.
 //
 // A CTA holds one tile of 128 outputs of a group and a range of its inputs, in steps of 128:
-//   * warps 0-7 copy the codes (cp.async, 8 bytes = 16 codes into each 16-byte slot of the
-//     SWIZZLE_128B layout: the tensor core reads 4-bit operands with 8 bytes of padding behind
-//     every 16 values) and the scale words, kAhead steps ahead, and run the epilogue;
-//   * warps 8-15 turn x into B's columns and scales;
-//   * one lane of warp 16 copies a step's scales into tensor memory and issues its four K = 32 MMAs.
+//   * warps 24 and 25: one thread each copies codes (pairs of steps: 128 bytes of a row) and x into
+//     shared memory as they lie (bulk tensor copies; what is past an end reads as 0);
+//   * warps 0-23 bring them into the tensor core's layouts: 16 codes into the first 8 bytes of each
+//     16-byte slot (it reads 4-bit operands with 8 bytes of padding behind every 16 values), rows of
+//     x into B's columns, scales into scale blocks; then they run the epilogue;
+//   * warps 26 and 27: one lane each copies a step's scales into tensor memory and issues its four
+//     K = 32 MMAs; each warp has its own sums.
 // A cluster of `split` CTAs shares a tile's inputs when there are fewer tiles than
-// multiprocessors; the partial tiles meet in distributed shared memory and are added in rank
-// order, so the result does not depend on timing.  Every mbarrier wait is bounded
+// multiprocessors; each sends its partial sums to the CTA that adds up the row of x, which adds
+// them in rank order, so the result does not depend on timing.  Every mbarrier wait is bounded
 // (LC_DEV_TIMEOUT).
+//
+// What bounds it is the chain through these roles, not memory: one row through 7168 x 4096 takes
+// 10.7 us in a graph (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.6 us for 14
+// steps of about 480 cycles (scales -> MMAs -> stage free), 1.7 us to join 4 CTAs, the rest is the
+// start of the next cluster.  32 rows through 8 groups of 4096 x 1024: 16.4 us, of which widening
+// x (16 conversions per 8 values, in every CTA that shares them) takes 850 cycles a step.
+// Tried: cp.async in place of the bulk copies (50 cycles of issue each: 12.7 and 18.4 us), one x
+// block per thread (1000 cycles a step), two steps per round of the issuing warps (11.0 and 16.7).
 #include <cuda.h>
 
 #include "lc_e4m3.cuh"
@@ -33,12 +43,9 @@ constexpr int kM = 128;                 // outputs per tile
 constexpr int kK = 128;                 // inputs per step
 constexpr int kTileA = kM * kK;         // bytes of A in shared memory (padded codes)
 constexpr int kSf = 512;                // bytes of a 128-row scale block: 32 rows of 4 words
-// warps by role
-// Warps of a role take steps in turn.  The turns divide kStages, so that a stage always has the same
-// ones and no barrier is waited for a round too early (and are at most kRawW, kRawX, likewise).
-constexpr int kTurns = 2, kTurnsX = 4;
-constexpr int kXT = 128;                // threads of a turn that turn x into B's columns
-constexpr int kWarpX = 4 * kTurns, kWarpCopy = kWarpX + kXT / 32 * kTurnsX, kWarpMma = kWarpCopy + 2;
+// 24 warps bring operands into the tensor core's layouts, in groups of 4 that take steps in turn
+constexpr int kWarpCopy = 24, kWarpMma = kWarpCopy + 2;
+constexpr int kTurns = 2;               // issuing warps, in turn
 constexpr int kThreads = 32 * (kWarpMma + kTurns);
 constexpr long kSpin = 1L << 20;  // a few seconds
 
@@ -48,16 +55,20 @@ template <int N, bool kMx>
 struct W4Smem {
   static constexpr int kTok = kMx ? N : N / 2;
   static constexpr int kUnits = kTok * (kMx ? 8 : 16);    // 16-byte units of x per step
+  // turns for the codes and for x: widening 16 or 32 BF16 rows costs more than spreading the codes
+  static constexpr int kTurnsW = !kMx && N >= 32 ? 2 : 4, kTurnsX = 6 - kTurnsW;
   static constexpr int kStages = 4;
-  static constexpr int kRawX = N <= 32 ? 6 : 4;
-  static constexpr int kRawW = N <= 32 ? 5 : 3;           // of two steps each: a row's 128 bytes
+  static constexpr int kRawX = kMx || N <= 16 ? 6 : N <= 32 ? 8 : 4;
+  static constexpr int kRawW = N <= 32 ? 6 : kMx ? 2 : 3;  // of two steps each: a row's 128 bytes
+  // Every place always has the same turns, so that no barrier is waited for a round too early
+  static_assert(kStages % kTurnsW == 0 && kStages % kTurnsX == 0 && kStages % kTurns == 0, "turns");
+  static_assert(2 * kRawW % kTurnsW == 0 && kRawX % kTurnsX == 0, "turns");
   static constexpr int kStage = kTileA + N * kK + 2 * kSf;
   static constexpr int kRawWBytes = kM * kK, kRawXBytes = kUnits * 16;
   static constexpr int kRing = kStages * kStage, kW = kRawW * kRawWBytes, kX = kRawX * kRawXBytes;
   // a CTA's share of the joined rows: (n_tok + split - 1) / split rows of `split` partial sums
   static constexpr int kPart = (kTok + 7) * kM * 4;
   static constexpr int kBytes = kRing + kW + kX + kPart + 1024;
-  static_assert(kStages % kTurns == 0 && kStages % kTurnsX == 0 && kRawX >= kTurnsX && kTurns == 2, "turns");
 };
 
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
@@ -121,7 +132,8 @@ template <int N, bool kMx>
 __global__ void __launch_bounds__(kThreads, 1)
     k_w4_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, lc_w4_proj_args a, int split, int tiles_g) {
   using L = W4Smem<N, kMx>;
-  constexpr int kStages = L::kStages, kTok = L::kTok;
+  constexpr int kStages = L::kStages, kTok = L::kTok, kTurnsW = L::kTurnsW, kTurnsX = L::kTurnsX;
+  constexpr int kWarpX = 4 * kTurnsW, kXT = 128;  // first warp that widens x, threads of a turn
   constexpr int kAcc = N + 16;                    // tensor-memory columns of an issuing warp: sums, scales
   constexpr uint32_t kCols = kTurns * kAcc <= 64 ? 64 : kTurns * kAcc <= 128 ? 128 : kTurns * kAcc <= 256 ? 256 : 512;
   extern __shared__ uint8_t smem_raw[];
@@ -223,9 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- the weights into A's layout (8-byte copies would land there by themselves, but ran
     // at a third of the rate): codes 32 seg .. + 15 and + 16 .. + 31 of a row are the first 8 bytes of
     // slots 2 seg and 2 seg + 1
-    // lanes take rows 4 apart in pairs: in the 128-byte swizzle their pieces fall into different banks
-    const int wt = tid & 127, seg = wt & 3, r0 = (wt & ~31) / 4 + (lane >> 3) + (lane & 4);
-    const uint32_t raw = su32(Wr) + sw128_off(r0, (warp >> 2) * 4 + seg);  // turn 0 has the first half of each pair
+    // four lanes a row, rows r and r ^ 5 side by side: in the 128-byte swizzles of both layouts their
+    // pieces fall into different banks
+    const int wt = tid & 127, seg = wt & 3, r0 = (wt & ~31) / 4 + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+    const uint32_t raw = su32(Wr) + sw128_off(r0, (warp >> 2 & 1) * 4 + seg);  // even steps have the first half of each pair
     const uint32_t d0 = su32(As) + sw128_off(r0, 2 * seg), d1 = su32(As) + sw128_off(r0, 2 * seg + 1);
     const uint32_t ds = su32(SFa) + sf_off(wt, 0);
     // the row's scales of a step, a turn ahead
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     uint32_t sw = scale_word(warp >> 2);
 #pragma unroll 1
-    for (int i = warp >> 2; i < n_step; i += kTurns) {
+    for (int i = warp >> 2; i < n_step; i += kTurnsW) {
       const int st = i % kStages, slot = i / 2 % L::kRawW;
       if (!wait(&wfull[slot], (i / 2 / L::kRawW) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
 #pragma unroll
@@ -250,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         st_shared8(d1 + st * kTileA + j * 4096, v.z, v.w);
       }
       st_shared4(ds + st * kSf, sw);
-      sw = scale_word(i + kTurns);
+      sw = scale_word(i + kTurnsW);
       mbar_arrive(su32(&wempty[slot]));
       fence_async_smem();
       mbar_arrive(su32(&full[st]));
