@@ -547,7 +547,7 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
   const int64_t all = static_cast<int64_t>(a.max_q) * geo.g;
   geo.decode = decode;
   geo.tc = !decode && all >= kTcRows;
-  geo.rows = geo.tc ? 256 : geo.g <= 8 ? 8 : 16;
+  geo.rows = geo.tc ? kv8_tc_rows(a.cache.D) : geo.g <= 8 ? 8 : 16;
   geo.row_tiles = static_cast<int>((all + geo.rows - 1) / geo.rows);
   geo.n_split = 1;
   int n = a.max_kv;

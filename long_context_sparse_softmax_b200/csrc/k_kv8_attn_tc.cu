@@ -29,10 +29,8 @@ namespace {
 constexpr int kTK = 128;                 // keys per tile
 constexpr int kHK = 64;                  // keys per product with Q and per softmax step
 constexpr int kRT = 128;                 // rows per row tile
-constexpr int kThreads = 512;
 constexpr float kHeadroom = 8.f;
 constexpr long kSpin = 1L << 20;         // a few seconds
-constexpr uint32_t kColO = 256;          // S_i at 128 i (two half tiles), O_i at 256 + 128 i
 constexpr int kHalf = kTK * 128;         // bytes of 128 rows x 64 F16 values (SWIZZLE_128B)
 
 struct Bars {
@@ -94,22 +92,35 @@ __device__ __forceinline__ void regs_dec() {
 // offset of chunk j (8 values) of half hf of row r in a tile of 128 rows
 __device__ __forceinline__ uint32_t tile_off(int r, int hf, int j) { return hf * kHalf + sw128_off(r, j); }
 
+// Row tiles of a CTA.  128 dims: two (tensor memory is full with S and O of both).  64 dims: one, and
+// two CTAs a multiprocessor: each starts and ends while the other computes (ragged windowed prefill of
+// 28 / 4 heads, 10 key tiles a CTA: 92 us with two row tiles, see below with one).
 template <int D>
-constexpr size_t smem_bytes() {
-  return 6 * static_cast<size_t>(kHalf) * (D / 64) + 1024;
-}
+struct Shape {
+  static constexpr int kT = D == 128 ? 2 : 1;
+  static constexpr int kSoft = 4 * kT;                     // softmax warps, then 4 that widen, then the issuing ones
+  static constexpr int kThreads = 32 * (kSoft + 8);
+  static constexpr int kPerSm = kT == 1 ? 2 : 1;
+  // registers a thread at launch, and by role: together what the CTA was launched with
+  static constexpr int kLaunch = kT == 2 ? 128 : 80, kRegSoft = kT == 2 ? 192 : 144, kRegWiden = kT == 2 ? 96 : 64, kRegIssue = 32;
+  static_assert(32 * kSoft * kRegSoft + 128 * (kRegWiden + kRegIssue) <= kThreads * kLaunch, "registers");
+  static constexpr uint32_t kColO = 128 * kT, kCols = 256 * kT;  // S_i at 128 i (two half tiles), O_i behind them
+  static constexpr size_t kSmem = (kT + 4) * static_cast<size_t>(kHalf) * (D / 64) + 1024;
+};
 
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
     k_kv8_attn_tc(lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
   constexpr int kTile = kHalf * (D / 64);  // bytes of a 128 x D F16 tile
   constexpr int kPR = D / 16;              // 16-code pieces per row
   constexpr int kIt = kTK * kPR / 128;     // pieces per converter thread
+  constexpr int kT = Shape<D>::kT, kSoft = Shape<D>::kSoft, kThreads = Shape<D>::kThreads;
+  constexpr uint32_t kColO = Shape<D>::kColO;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* Qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* Ks = Qs + 2 * kTile;
+  uint8_t* Ks = Qs + kT * kTile;
   uint8_t* Vs = Ks + 2 * kTile;
   __shared__ float4 s_sc[4][8];  // per 16 keys of a tile: 2^ek, ev, 2^-ev (ring of 4 tiles)
   __shared__ uint32_t s_tmem;
@@ -129,10 +140,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int q0 = __ldg(a.q_start + s);
   const int nq = min(__ldg(a.q_start + s + 1) - q0, a.max_q);
-  const int64_t row0 = static_cast<int64_t>(rt) * (2 * kRT);
+  const int64_t row0 = static_cast<int64_t>(rt) * (kT * kRT);
   const int64_t all_rows = static_cast<int64_t>(nq) * geo.g;
   if (nq <= 0 || row0 >= all_rows) return;
-  const int n_row = static_cast<int>(min(static_cast<int64_t>(2 * kRT), all_rows - row0));
+  const int n_row = static_cast<int>(min(static_cast<int64_t>(kT * kRT), all_rows - row0));
   const int n_act = n_row > kRT ? 2 : 1;
   const int p0 = __ldg(a.q_pos0 + s);
   const int kv_all = __ldg(a.kv_len + s);
@@ -160,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-  if (warp == 12) tmem_alloc(su32(&s_tmem), 512);
+  if (warp == kSoft + 4) tmem_alloc(su32(&s_tmem), Shape<D>::kCols);
   if (tid == 0) {
     s_abort = s_nan = 0;
     for (int i = 0; i < 2; ++i) {
@@ -183,14 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tm = s_tmem;
 
-  const int i = warp < 8 ? warp >> 2 : warp - 12;  // row tile of a softmax or issuing warp
-  const int r = tid & 255;                         // softmax: row of the CTA
+  const int i = warp < kSoft ? warp >> 2 : warp - (kSoft + 4);  // row tile of a softmax or issuing warp
+  const int r = tid;                               // softmax: row of the CTA
   float R = -INFINITY, l = 0.f;
   bool good = true;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
 
-  if (warp < 8) {
-    regs_inc<192>();
+  if (warp < kSoft) {
+    regs_inc<Shape<D>::kRegSoft>();
     if (i < n_act) {
       // ---------------- Q: the row, scaled by a power of two into F16's range (k_kv8_attn.cu)
       float f_row;
@@ -271,8 +282,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (edge) {
 #pragma unroll
-            for (int j = 0; j < kHK; ++j)
-              if (j < d_lo || j >= d_hi) y[j / 32][j % 32] = 0xff800000u;
+            for (int x = 0; x < 2; ++x) {
+              // bit j: the row sees key 32 x + j of the half tile
+              const int lo = min(max(d_lo - 32 * x, 0), 32), hi = min(max(d_hi - 32 * x, 0), 32);
+              const uint32_t below = hi < 32 ? (1u << hi) - 1 : 0xffffffffu, from = lo < 32 ? 0xffffffffu << lo : 0u;
+              const uint32_t see = below & from;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see & (1u << j))) y[x][j] = 0xff800000u;
+            }
           }
 #pragma unroll
           for (int g = 0; g < kHK / 16; ++g) {
@@ -375,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before();
     }
-  } else if (warp < 12) {
+  } else if (warp < kSoft + 4) {
     // ---------------- codes -> F16 tiles
-    regs_dec<96>();
-    const int cw = warp - 8;
+    regs_dec<Shape<D>::kRegWiden>();
+    const int cw = warp - kSoft;
     // a warp's 32 pieces are whole rows (512 bytes); the eight lanes of a 16-byte store phase take four
     // pieces of two neighbouring rows, whose chunks fall into different banks
     const int piece = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
@@ -473,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_bar(1, kThreads);
   } else {
     // ---------------- products of row tile i
-    regs_dec<32>();
+    regs_dec<Shape<D>::kRegIssue>();
     if (i < n_act) {
       const bool one = elect_one();
       const uint32_t id_s = (1u << 4) | (static_cast<uint32_t>(kHK >> 3) << 17) | (static_cast<uint32_t>(kRT >> 4) << 24);
@@ -526,18 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_bar(1, kThreads);
   }
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tm, 512);
+  if (warp == kSoft + 4) tmem_dealloc(tm, Shape<D>::kCols);
 }
 
 cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,
                                cudaStream_t st) {
-  auto go = [&](auto kernel, size_t smem) {
+  auto go = [&](auto kernel, int threads, size_t smem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, st>>>(a, geo, ws_o, ws_ml);
+    kernel<<<grid, threads, smem, st>>>(a, geo, ws_o, ws_ml);
     return cudaGetLastError();
   };
-  return a.cache.D == 128 ? go(k_kv8_attn_tc<128>, smem_bytes<128>()) : go(k_kv8_attn_tc<64>, smem_bytes<64>());
+  return a.cache.D == 128 ? go(k_kv8_attn_tc<128>, Shape<128>::kThreads, Shape<128>::kSmem)
+                          : go(k_kv8_attn_tc<64>, Shape<64>::kThreads, Shape<64>::kSmem);
 }
 
 }  // namespace lc

@@ -100,6 +100,8 @@ struct Kv8Geom {
   int decode;     // query s belongs to sequence s
 };
 
+// rows of a CTA of k_kv8_attn_tc
+inline int kv8_tc_rows(int D) { return D == 128 ? 256 : 128; }
 cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,
                                cudaStream_t st);
 
