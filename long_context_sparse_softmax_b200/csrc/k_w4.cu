@@ -55,11 +55,14 @@ template <int N, bool kMx>
 struct W4Smem {
   static constexpr int kTok = kMx ? N : N / 2;
   static constexpr int kUnits = kTok * (kMx ? 8 : 16);    // 16-byte units of x per step
-  // turns for the codes and for x: widening 16 or 32 BF16 rows costs more than spreading the codes
-  static constexpr int kTurnsW = !kMx && N >= 32 ? 2 : 4, kTurnsX = 6 - kTurnsW;
+  // turns for the codes (128 threads each) and for x (kXT threads each; what is enough for a few rows or
+  // for MXFP8 would hold up 16 or 32 rows of BF16)
+  static constexpr bool kWide = !kMx && N >= 32;
+  static constexpr int kTurnsW = kWide ? 2 : 4, kTurnsX = 4, kXT = kWide ? 128 : 64;
+  static_assert(4 * kTurnsW + kXT / 32 * kTurnsX == kWarpCopy, "warps");
   static constexpr int kStages = 4;
-  static constexpr int kRawX = kMx || N <= 16 ? 6 : N <= 32 ? 8 : 4;
-  static constexpr int kRawW = N <= 32 ? 6 : kMx ? 2 : 3;  // of two steps each: a row's 128 bytes
+  static constexpr int kRawX = N <= 32 ? 8 : 4;
+  static constexpr int kRawW = N <= 16 ? 6 : N <= 32 ? 4 : kMx ? 2 : 3;  // of two steps each: a row's 128 bytes
   // Every place always has the same turns, so that no barrier is waited for a round too early
   static_assert(kStages % kTurnsW == 0 && kStages % kTurnsX == 0 && kStages % kTurns == 0, "turns");
   static_assert(2 * kRawW % kTurnsW == 0 && kRawX % kTurnsX == 0, "turns");
@@ -74,11 +77,6 @@ struct W4Smem {
 __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t ld_shared4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared16(uint32_t a, uint4 v) {
@@ -133,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_w4_proj(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, lc_w4_proj_args a, int split, int tiles_g) {
   using L = W4Smem<N, kMx>;
   constexpr int kStages = L::kStages, kTok = L::kTok, kTurnsW = L::kTurnsW, kTurnsX = L::kTurnsX;
-  constexpr int kWarpX = 4 * kTurnsW, kXT = 128;  // first warp that widens x, threads of a turn
+  constexpr int kWarpX = 4 * kTurnsW, kXT = L::kXT;  // first warp that widens x
   constexpr int kAcc = N + 16;                    // tensor-memory columns of an issuing warp: sums, scales
   constexpr uint32_t kCols = kTurns * kAcc <= 64 ? 64 : kTurns * kAcc <= 128 ? 128 : kTurns * kAcc <= 256 ? 256 : 512;
   extern __shared__ uint8_t smem_raw[];
