@@ -11,7 +11,6 @@
 // result does not depend on the launch shape.
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
-#include "lc_ptx.cuh"
 
 namespace lc {
 
@@ -146,12 +145,13 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(lc_kv8_append_args a, u
 namespace {
 
 template <bool kF32>
-void launch(const lc_kv8_append_args& a, unsigned grid, uint32_t max_blk, cudaStream_t st) {
+cudaError_t launch(const lc_kv8_append_args& a, unsigned grid, uint32_t max_blk, cudaStream_t st) {
+  auto go = [&](auto kernel) { return launch_ex(kernel, dim3(grid), dim3(kThreads), 0, st, false, 1, a, max_blk); };  // nothing to set up ahead
   const int groups = a.cache.bt * a.cache.D / 8;  // 128 .. 2048
-  if (groups <= kThreads) k_kv8_append<kF32, 1><<<grid, kThreads, 0, st>>>(a, max_blk);
-  else if (groups <= 2 * kThreads) k_kv8_append<kF32, 2><<<grid, kThreads, 0, st>>>(a, max_blk);
-  else if (groups <= 4 * kThreads) k_kv8_append<kF32, 4><<<grid, kThreads, 0, st>>>(a, max_blk);
-  else k_kv8_append<kF32, 8><<<grid, kThreads, 0, st>>>(a, max_blk);
+  if (groups <= kThreads) return go(k_kv8_append<kF32, 1>);
+  if (groups <= 2 * kThreads) return go(k_kv8_append<kF32, 2>);
+  if (groups <= 4 * kThreads) return go(k_kv8_append<kF32, 4>);
+  return go(k_kv8_append<kF32, 8>);
 }
 
 }  // namespace
@@ -162,9 +162,8 @@ cudaError_t launch_kv8_append(const lc_kv8_append_args& a, cudaStream_t st) {
   const int64_t max_blk = 1 + (static_cast<int64_t>(a.max_tok) + bt - 2) / bt;
   const int64_t grid = max_blk * 2 * a.num_seqs * a.cache.H_kv;
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (a.in_fmt == LC_FMT_F32) launch<true>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
-  else launch<false>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
-  return cudaGetLastError();
+  if (a.in_fmt == LC_FMT_F32) return launch<true>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
+  return launch<false>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
 }
 
 }  // namespace lc

@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int bt_log = __ffs(c.bt) - 1;
+  pdl_wait();
+  pdl_trigger();
   // 32-bit divisions: what a CTA does besides its keys counts when a split has 512 of them
   uint32_t u = blockIdx.x;
   const int split = static_cast<int>(u % static_cast<uint32_t>(geo.n_split));
@@ -445,6 +447,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ float s_o[kCombineWarps][D];
   pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t orow = blockIdx.x;
   const int q = static_cast<int>(blockIdx.x / static_cast<uint32_t>(a.H)), head = static_cast<int>(blockIdx.x % static_cast<uint32_t>(a.H));
@@ -572,14 +575,12 @@ cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t s
   const size_t rows = static_cast<size_t>(a.n_q) * a.H;
   float* ws_o = static_cast<float*>(a.workspace);
   float2* ws_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align16(rows * geo.n_split * D * 4));
-  if (geo.tc) {
-    const cudaError_t e = launch_kv8_attn_tc(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st);
-    if (e != cudaSuccess) return e;
-  } else if (geo.rows == 8) k_kv8_attn<D, 1><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
-  else k_kv8_attn<D, 2><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, geo, ws_o, ws_ml);
-  if (geo.n_split == 1) return cudaGetLastError();
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  auto go = [&](auto kernel) {
+    return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, true, 1, a, geo, ws_o, ws_ml);
+  };
+  const cudaError_t e = geo.tc ? launch_kv8_attn_tc(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st)
+                        : geo.rows == 8 ? go(k_kv8_attn<D, 1>) : go(k_kv8_attn<D, 2>);
+  if (e != cudaSuccess || geo.n_split == 1) return e;
   return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>(rows)), dim3(32 * kCombineWarps), 0, st, true, 1, a, geo,
                    static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));
 }

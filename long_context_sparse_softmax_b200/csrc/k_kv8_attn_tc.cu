@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
   __shared__ int s_abort, s_nan;
   __shared__ __align__(8) Bars bars;
 
+  pdl_wait();
+  pdl_trigger();
   const lc_kv8_cache& c = a.cache;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   int64_t u = blockIdx.x;
@@ -552,8 +554,7 @@ cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, un
   auto go = [&](auto kernel, int threads, size_t smem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, st>>>(a, geo, ws_o, ws_ml);
-    return cudaGetLastError();
+    return launch_ex(kernel, dim3(grid), dim3(threads), smem, st, true, 1, a, geo, ws_o, ws_ml);
   };
   return a.cache.D == 128 ? go(k_kv8_attn_tc<128>, Shape<128>::kThreads, Shape<128>::kSmem)
                           : go(k_kv8_attn_tc<64>, Shape<64>::kThreads, Shape<64>::kSmem);

@@ -113,6 +113,10 @@ __global__ void __launch_bounds__(kThreads, kV <= 4 ? 3 : 1) k_add_rms_norm(lc_a
     mbar_init(su32(&wfull), 1);
     fence_mbar_init();
   }
+  // what was set up so far overlapped the kernel before; its results are there now, and all before it
+  // (only then may the next kernel start: it can rely on this one's inputs, too)
+  pdl_wait();
+  pdl_trigger();
   __syncthreads();
 
   if (warp == kWarps) {
@@ -277,8 +281,7 @@ cudaError_t launch_norm(const lc_add_rms_norm_args& a, const NormGeom& geo, unsi
   auto go = [&](auto kernel) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, st>>>(a, geo);
-    return cudaGetLastError();
+    return launch_ex(kernel, dim3(grid), dim3(kThreads), smem, st, true, 1, a, geo);
   };
   if (a.out_fmt == LC_FMT_F32) return go(k_add_rms_norm<kF32, kV, LC_FMT_F32>);
   if (a.out_fmt == LC_FMT_BF16) return go(k_add_rms_norm<kF32, kV, LC_FMT_BF16>);

@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = tid; i < kStages * kSf / 4; i += kThreads) reinterpret_cast<uint32_t*>(SFb)[i] = 0x7f7f7f7fu;
   fence_async_smem();
   fence_before();
+  // what was set up so far overlapped the kernel before; its results are there now, and all before it
+  // (only then may the next kernel start: it can rely on this one's inputs, too)
+  pdl_wait();
+  pdl_trigger();
   __syncthreads();
   fence_after();
   const uint32_t tm = s_tmem;
@@ -493,7 +497,7 @@ cudaError_t launch_w4(const lc_w4_proj_args& a, int split, int tiles_g, cudaStre
   const dim3 grid(static_cast<unsigned>(a.G * tiles_g * split), static_cast<unsigned>((a.n_q + kTok - 1) / kTok));
   const cudaError_t e = cudaFuncSetAttribute(k_w4_proj<N, kMx>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const cudaError_t r = launch_ex(k_w4_proj<N, kMx>, grid, dim3(kThreads), smem, st, false, split, map_w, map_x, a, split, tiles_g);
+  const cudaError_t r = launch_ex(k_w4_proj<N, kMx>, grid, dim3(kThreads), smem, st, true, split, map_w, map_x, a, split, tiles_g);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 
