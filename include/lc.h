@@ -579,7 +579,7 @@ lc_status lc_kv8_append(const lc_kv8_append_args* a, void* stream);
 
 /* kv8_attn — attention of H query heads over the 8-bit cache; H / H_kv consecutive heads
  * share one cache head.  Query i of sequence s sits at p = q_pos0[s] + i and sees the cached
- * tokens t <= p, t < kv_len[s], and with W > 0 only t > p - W:
+ * tokens t <= p, t < kv_len[s], and with W > 0 only t > p - W (positions are below 2^31):
  *   l_t = scale <q_h, k_t>, M = max(sink_h, max l), Z = e^(sink_h - M) + sum e^(l_t - M),
  *   o = sum e^(l_t - M) v_t / Z, lse = M + ln Z   (sink NULL: no sink term).
  * A query that sees no token gets o = 0 and lse = sink_h (-inf without a sink).  out and lse
@@ -587,7 +587,8 @@ lc_status lc_kv8_append(const lc_kv8_append_args* a, void* stream);
  * sees makes its outputs NaN; what it does not see never reaches it.
  * Prefill: any number of queries per sequence.  Decode: one query per sequence (n_q ==
  * num_seqs, q_start[s] = s).  Both split the keys over CTAs where there are few rows, and then
- * need a workspace of lc_kv8_attn_workspace_bytes(a, decode) bytes (host fields only). */
+ * need a workspace of lc_kv8_attn_workspace_bytes(a, decode) bytes (host fields only; it holds
+ * nothing between calls).  A decode result depends on its own sequence alone, not on the batch. */
 typedef struct lc_kv8_attn_args {
   lc_kv8_cache cache;      /* read only */
   int32_t H;               /* query heads: multiple of H_kv */

@@ -1,24 +1,30 @@
 // kv8_attn for many query rows (prefill) on the 5th-generation tensor cores (tcgen05, F16 operands,
 // FP32 accumulators in tensor memory).  The same arithmetic as k_kv8_attn.cu: see lc_kv8.cuh.
 //
-// A CTA holds 256 rows of one sequence and shared head (row r: query r / g, head r % g of the
-// group) as two tiles of 128 rows that share every key tile of 128 tokens:
-//   S_i = Q_i K^T   M = 128 rows, N = 128 keys, both K-major in shared memory;
+// A CTA holds one or two tiles (kT) of 128 rows of one sequence and shared head (row r: query r / g,
+// head r % g of the group), which share every key tile of 128 tokens:
+//   S_i = Q_i K^T   M = 128 rows, N = 64 keys (half tiles, two of them per row tile), both K-major in
+//                   shared memory;
 //   P_i             F16 weights, written over S_i's columns of tensor memory;
 //   O_i += P_i V    A = P_i in tensor memory, B = V (keys x dims, dims contiguous: MN-major).
-// The codes are widened to F16 (exact) once per CTA, so 256 rows share that work and the row's
-// softmax keeps the precision that it has with few rows.  While one row tile's softmax runs, the
-// tensor core works on the other's products.
+// The codes are widened to F16 (exact) once per CTA, and the row's softmax keeps the precision that
+// it has with few rows.  S of a half tile is computed while the softmax works on the half before, and
+// one row tile's (or CTA's) softmax runs while the tensor core works on the other's products.
 //
-// Warps 0-3 and 4-7: softmax of row tile 0 and 1, a thread per row (its sums need no shuffles).
-// Warps 8-11: fetch codes into registers a tile ahead, widen them into the two-stage rings of K
-// and V.  Warps 12 and 13: lane 0 issues the products of row tile 0 and 1.
-// (Warps 14 and 15 only complete their warpgroup.)  Registers, a thread: 192 for softmax, 96 to
-// widen, 32 to issue: 256 * 192 + 128 * 96 + 128 * 32 = 512 * 128, what the CTA was launched with.
-// A softmax thread computes its tile's weights with the reference R it has; only when one would
+// Warps 0 .. 4 kT - 1: softmax, a thread per row (its sums need no shuffles).  The next 4: fetch codes
+// into registers a tile ahead, widen them into the two-stage rings of K and V.  The next kT: one lane
+// issues the products of a row tile.  (The others only complete their warpgroup.)
+// A softmax thread computes its half tile's weights with the reference R it has; only when one would
 // pass 2^8 does R move, O is rescaled in tensor memory and the weights are computed again (the
-// first tile, and rarely after it).  Tiles whose keys every row sees skip the mask.
+// first half tile, and rarely after it).  Half tiles whose keys every row sees skip the mask.
 // Every wait on an mbarrier is bounded (LC_DEV_TIMEOUT).
+//
+// What bounds it: the exponentials (16 a cycle on a multiprocessor: 2048 cycles per 256 x 128 tile, as
+// many as its products take) and the latency of each softmax step; a tile takes about 4000 cycles.
+// 2048 queries at the end of 8192 tokens, 64 / 8 heads of 128 dims: 498 us, 965 TFLOP/s (57 % of the
+// measured F16 rate; 512 CTAs are 3.46 rounds of 148, run as 4).  On the way there: a mma.sync kernel with
+// 8 rows a tile 4960 us; 256 rows on tcgen05 1190; packed FP32 pairs and a uniform issuing warp 734; half
+// tiles ahead of the softmax 545; cheaper widening and masks 520.
 #include "lc_e4m3.cuh"
 #include "lc_kv8.cuh"
 
@@ -94,7 +100,7 @@ __device__ __forceinline__ uint32_t tile_off(int r, int hf, int j) { return hf *
 
 // Row tiles of a CTA.  128 dims: two (tensor memory is full with S and O of both).  64 dims: one, and
 // two CTAs a multiprocessor: each starts and ends while the other computes (ragged windowed prefill of
-// 28 / 4 heads, 10 key tiles a CTA: 92 us with two row tiles, see below with one).
+// 28 / 4 heads, 10 key tiles a CTA: 92 us with two row tiles a CTA, 83 us with one).
 template <int D>
 struct Shape {
   static constexpr int kT = D == 128 ? 2 : 1;

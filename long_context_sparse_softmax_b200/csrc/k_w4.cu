@@ -23,12 +23,15 @@
 // (LC_DEV_TIMEOUT).
 //
 // What bounds it is the chain through these roles, not memory: one row through 7168 x 4096 takes
-// 10.7 us in a graph (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.6 us for 14
-// steps of about 480 cycles (scales -> MMAs -> stage free), 1.7 us to join 4 CTAs, the rest is the
-// start of the next cluster.  32 rows through 8 groups of 4096 x 1024: 16.4 us, of which widening
-// x (16 conversions per 8 values, in every CTA that shares them) takes 850 cycles a step.
+// 9.1 us in a graph (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.5 us for 14
+// steps (scales -> MMAs -> stage free), 1.4 us to join 4 CTAs, the rest is the start of the next
+// cluster.  32 rows through 8 groups of 4096 x 1024: 15.3 us, of which widening x (16 conversions per
+// 8 values, in every CTA that shares them) takes 850 cycles a step; 17 rows of MXFP8 through
+// 7168 x 7000: 14.3 us.
 // Tried: cp.async in place of the bulk copies (50 cycles of issue each: 12.7 and 18.4 us), one x
-// block per thread (1000 cycles a step), two steps per round of the issuing warps (11.0 and 16.7).
+// block per thread (1000 cycles a step), two steps per round of the issuing warps (11.0 and 16.7, when
+// this took 10.7 and 16.4), BF16 weights by table lookup for the warps' own matrix instruction (9.5 us
+// for one row, then 10.7 here, and 18.4: bound by the integer pipe).
 #include <cuda.h>
 
 #include "lc_e4m3.cuh"
