@@ -549,8 +549,11 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_
 namespace {
 
 // From this many rows per (sequence, shared head) on, a call takes the tensor-memory kernel: its tiles have
-// 128 rows whether they are full or not, k_kv8_attn reads the keys again for every 8 (or 16) rows
-constexpr int kTcRows = 64;
+// 128 rows whether they are full or not, k_kv8_attn reads the keys again for every 8 (or 16) rows.
+// Measured (us, k_kv8_attn / k_kv8_attn_tc), 8 heads of 128 dims, 8 query heads each: one sequence of 8192
+// tokens 17.0 / 17.2 at 16 rows, 20.6 / 19.1 at 32, 34 / 20 at 64; of 65536 60 / 66, 105 / 67, 177 / 68; eight of
+// 8192 37 / 68, 69 / 72, 127 / 74.  8 heads of 64 dims, 4 query heads each, eight of 8192: 44 / 44 at 32, 60 / 46 at 64.
+constexpr int kTcRows = 32;
 
 // Splits that any row tile of the call can have.
 Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
@@ -565,9 +568,9 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
   int n = a.max_kv;
   if (a.W > 0 && a.W + a.max_q - 1 < n - 16) n = a.W + a.max_q - 1 + 16;
   if (geo.tc) {
-    // fewer CTAs than multiprocessors: split the keys, at least 4 tiles of 128 each
+    // fewer CTAs than the device holds at once: split the keys, at least 4 tiles of 128 each
     const int64_t ctas = static_cast<int64_t>(geo.row_tiles) * a.cache.H_kv * a.num_seqs;
-    const int64_t fill = sm_count() / ctas;
+    const int64_t fill = sm_count() * (a.cache.D == 128 ? 1 : 2) / ctas;
     geo.n_split = static_cast<int>(max(int64_t{1}, min(fill, static_cast<int64_t>(n) / 512)));
   } else {
     geo.n_split = kv8_split_bound(n, a.cache.H_kv);
