@@ -14,13 +14,14 @@
 // Warps 0 .. 4 kT - 1: softmax, a thread per row (its sums need no shuffles).  The next 4: fetch codes
 // into registers a tile ahead, widen them into the two-stage rings of K and V.  The next kT: one lane
 // issues the products of a row tile.  (The others only complete their warpgroup.)
-// A softmax thread computes its half tile's weights with the reference R it has; only when one would
-// pass 2^8 does R move, O is rescaled in tensor memory and the weights are computed again (the
+// A softmax thread computes its half tile's weights with the reference R it has; only when their sum
+// passes 2^12 does R move to the largest logit, O is rescaled in tensor memory and the weights are computed again (the
 // first half tile, and rarely after it).  Half tiles whose keys every row sees skip the mask.
 // Every wait on an mbarrier is bounded (LC_DEV_TIMEOUT).
 //
 // What bounds it: the exponentials (16 a cycle on a multiprocessor: 2048 cycles per 256 x 128 tile, as
-// many as its products take) and the latency of each softmax step; a tile takes about 4000 cycles.
+// many as its products take) and the latency of each softmax step; a tile takes about 4000 cycles, 2950
+// of them for the weights.
 // 2048 queries at the end of 8192 tokens, 64 / 8 heads of 128 dims: 498 us, 965 TFLOP/s (57 % of the
 // measured F16 rate; 512 CTAs are 3.46 rounds of 148, run as 4).  On the way there: a mma.sync kernel with
 // 8 rows a tile 4960 us; 256 rows on tcgen05 1190; packed FP32 pairs and a uniform issuing warp 734; half
@@ -35,7 +36,7 @@ namespace {
 constexpr int kTK = 128;                 // keys per tile
 constexpr int kHK = 64;                  // keys per product with Q and per softmax step
 constexpr int kRT = 128;                 // rows per row tile
-constexpr float kHeadroom = 8.f;
+constexpr float kMaxSum = 4096.f;         // of a half tile's weights before R moves
 constexpr long kSpin = 1L << 20;         // a few seconds
 constexpr int kHalf = kTK * 128;         // bytes of 128 rows x 64 F16 values (SWIZZLE_128B)
 
@@ -100,7 +101,8 @@ __device__ __forceinline__ uint32_t tile_off(int r, int hf, int j) { return hf *
 
 // Row tiles of a CTA.  128 dims: two (tensor memory is full with S and O of both).  64 dims: one, and
 // two CTAs a multiprocessor: each starts and ends while the other computes (ragged windowed prefill of
-// 28 / 4 heads, 10 key tiles a CTA: 92 us with two row tiles a CTA, 83 us with one).
+// 28 / 4 heads, 10 key tiles a CTA: 92 us with two row tiles a CTA, 83 us with one, 80 us without a maximum
+// per key).
 template <int D>
 struct Shape {
   static constexpr int kT = D == 128 ? 2 : 1;
@@ -265,61 +267,72 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
           break;
         }
         fence_after();
-        // y = x + ev - R and the weights 2^y
+        uint32_t y[2][32];
+        tmem_ld32(ts + bf * kHK, y[0]);
+        tmem_ld32(ts + bf * kHK + 32, y[1]);
+        tmem_wait_ld();
+        // y = x + ev - R
+        const float Ru = R == -INFINITY ? 0.f : R;
+#pragma unroll
+        for (int g = 0; g < kHK / 16; ++g) {
+          const float2 sc = ld_shared2(&s_sc[t & 3][bf * 4 + g]);
+          const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
+          uint32_t* v = y[g / 2] + (g & 1) * 16;
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) fma2_regs(v[j], v[j + 1], fk, off);
+        }
+        bool sees = r < n_row;  // a key of the half tile
+        if (edge) {
+          const int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the half tile
+          sees = d_lo < kHK && d_hi > 0 && d_lo < d_hi;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            // bit j: the row sees key 32 x + j of the half tile
+            const int lo = min(max(d_lo - 32 * x, 0), 32), hi = min(max(d_hi - 32 * x, 0), 32);
+            const uint32_t below = hi < 32 ? (1u << hi) - 1 : 0xffffffffu, from = lo < 32 ? 0xffffffffu << lo : 0u;
+            const uint32_t see = below & from;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(see & (1u << j))) y[x][j] = 0xff800000u;
+          }
+        }
+        // the weights 2^y, their sum, and the part of l that is theirs
         uint32_t pk[kHK / 2];
         float ls, al = 1.f;
         bool again = false;
         do {
           const bool second = again;
-          const float Ru = R == -INFINITY ? 0.f : R;
-          int d_lo = r_lo - t0, d_hi = r_hi - t0;  // the row's keys within the half tile
-          asm volatile("" : "+r"(d_lo), "+r"(d_hi));
-          float ymax = -INFINITY;
+          float sum = 0.f;
           ls = 0.f;
-          uint32_t y[2][32];
-          tmem_ld32(ts + bf * kHK, y[0]);
-          tmem_ld32(ts + bf * kHK + 32, y[1]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int g = 0; g < kHK / 16; ++g) {
-            const float2 sc = ld_shared2(&s_sc[t & 3][bf * 4 + g]);
-            const uint64_t fk = pack2(f_row * sc.x, f_row * sc.x), off = pack2(sc.y - Ru, sc.y - Ru);
-            uint32_t* v = y[g / 2] + (g & 1) * 16;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) fma2_regs(v[j], v[j + 1], fk, off);
-          }
-          if (edge) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // bit j: the row sees key 32 x + j of the half tile
-              const int lo = min(max(d_lo - 32 * x, 0), 32), hi = min(max(d_hi - 32 * x, 0), 32);
-              const uint32_t below = hi < 32 ? (1u << hi) - 1 : 0xffffffffu, from = lo < 32 ? 0xffffffffu << lo : 0u;
-              const uint32_t see = below & from;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see & (1u << j))) y[x][j] = 0xff800000u;
-            }
-          }
 #pragma unroll
           for (int g = 0; g < kHK / 16; ++g) {
             const uint32_t* v = y[g / 2] + (g & 1) * 16;
             uint64_t gs = 0;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
-              const float y0 = __uint_as_float(v[j]), y1 = __uint_as_float(v[j + 1]);
-              ymax = fmaxf(ymax, fmaxf(y0, y1));
-              const float w0 = ex2(y0), w1 = ex2(y1);
+              const float w0 = ex2(__uint_as_float(v[j])), w1 = ex2(__uint_as_float(v[j + 1]));
               gs = add2(gs, pack2(w0, w1));
               const __half2 hv = __floats2half2_rn(w0, w1);
               pk[g * 8 + j / 2] = *reinterpret_cast<const uint32_t*>(&hv);
             }
-            ls = fmaf(sum2(gs), ld_shared1(&s_sc[t & 3][bf * 4 + g].z), ls);
+            const float s16 = sum2(gs);
+            sum += s16;
+            ls = fmaf(s16, ld_shared1(&s_sc[t & 3][bf * 4 + g].z), ls);
           }
-          const bool need = !second && (R == -INFINITY ? ymax > -INFINITY : ymax > kHeadroom);
+          // R is the largest logit when it is set; a sum says whether a weight has come near F16's end since
+          const bool need = !second && (R == -INFINITY ? sees : sum > kMaxSum);
           again = __any_sync(0xffffffffu, need);
-          if (need) {
-            al = ref_factor(R, Ru + ymax);
-            R = Ru + ymax;
+          if (again) {
+            float ymax = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kHK; ++j) ymax = fmaxf(ymax, __uint_as_float(y[j / 32][j % 32]));
+            const float up = need && ymax > -INFINITY ? ymax : 0.f;
+            if (need && ymax > -INFINITY) {
+              al = ref_factor(R, Ru + up);
+              R = Ru + up;
+            }
+#pragma unroll
+            for (int j = 0; j < kHK; ++j) y[j / 32][j % 32] = __float_as_uint(__uint_as_float(y[j / 32][j % 32]) - up);
           }
         } while (again);
         if (__any_sync(0xffffffffu, al != 1.f) && hh > 0) {
