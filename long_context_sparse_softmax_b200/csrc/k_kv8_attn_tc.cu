@@ -568,15 +568,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
   if (warp == kSoft + 4) tmem_dealloc(tm, Shape<D>::kCols);
 }
 
+template <int D>
+static cudaError_t launch_d(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml, cudaStream_t st) {
+  const cudaError_t e = allow_smem<k_kv8_attn_tc<D>>(Shape<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_kv8_attn_tc<D>, dim3(grid), dim3(Shape<D>::kThreads), Shape<D>::kSmem, st, true, 1, a, geo, ws_o, ws_ml);
+}
+
 cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,
                                cudaStream_t st) {
-  auto go = [&](auto kernel, int threads, size_t smem) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_ex(kernel, dim3(grid), dim3(threads), smem, st, true, 1, a, geo, ws_o, ws_ml);
-  };
-  return a.cache.D == 128 ? go(k_kv8_attn_tc<128>, Shape<128>::kThreads, Shape<128>::kSmem)
-                          : go(k_kv8_attn_tc<64>, Shape<64>::kThreads, Shape<64>::kSmem);
+  return a.cache.D == 128 ? launch_d<128>(a, geo, grid, ws_o, ws_ml, st) : launch_d<64>(a, geo, grid, ws_o, ws_ml, st);
 }
 
 }  // namespace lc

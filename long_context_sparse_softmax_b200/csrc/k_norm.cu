@@ -278,16 +278,22 @@ __global__ void __launch_bounds__(kThreads, kV <= 4 ? 3 : 1) k_add_rms_norm(lc_a
 
 namespace {
 
+constexpr size_t kRoom = 216 * 1024;  // dynamic shared memory of a multiprocessor that the CTAs share
+
+template <auto kKernel>
+cudaError_t launch_one(const lc_add_rms_norm_args& a, const NormGeom& geo, unsigned grid, size_t smem, cudaStream_t st) {
+  if (smem > 46 * 1024) {  // 48 KB with the static part need no asking
+    const cudaError_t e = allow_smem<kKernel>(kRoom);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_ex(kKernel, dim3(grid), dim3(kThreads), smem, st, true, 1, a, geo);
+}
+
 template <bool kF32, int kV>
 cudaError_t launch_norm(const lc_add_rms_norm_args& a, const NormGeom& geo, unsigned grid, size_t smem, cudaStream_t st) {
-  auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
-    if (e != cudaSuccess) return e;
-    return launch_ex(kernel, dim3(grid), dim3(kThreads), smem, st, true, 1, a, geo);
-  };
-  if (a.out_fmt == LC_FMT_F32) return go(k_add_rms_norm<kF32, kV, LC_FMT_F32>);
-  if (a.out_fmt == LC_FMT_BF16) return go(k_add_rms_norm<kF32, kV, LC_FMT_BF16>);
-  return go(k_add_rms_norm<kF32, kV, LC_FMT_MXFP8>);
+  if (a.out_fmt == LC_FMT_F32) return launch_one<k_add_rms_norm<kF32, kV, LC_FMT_F32>>(a, geo, grid, smem, st);
+  if (a.out_fmt == LC_FMT_BF16) return launch_one<k_add_rms_norm<kF32, kV, LC_FMT_BF16>>(a, geo, grid, smem, st);
+  return launch_one<k_add_rms_norm<kF32, kV, LC_FMT_MXFP8>>(a, geo, grid, smem, st);
 }
 
 template <bool kF32>
@@ -314,13 +320,13 @@ cudaError_t launch_add_rms_norm(const lc_add_rms_norm_args& a, cudaStream_t st) 
   // as many CTAs per multiprocessor as keep two stages each, then as many stages as fit
   const size_t stage = row * tile_rows * (a.res ? 2 : 1);
   const size_t w = a.w ? static_cast<size_t>(a.d) * (a.w_fmt == LC_FMT_F32 ? 4 : 2) : 0;
-  constexpr size_t kRoom = 216 * 1024;
   size_t per_sm = 3;
   while (per_sm > 1 && per_sm * (w + 2 * stage) > kRoom) --per_sm;
   const size_t fit = (kRoom / per_sm - w) / stage;
-  geo.stages = static_cast<int>(fit < kMaxStages ? fit : kMaxStages);
   const int64_t most = static_cast<int64_t>(per_sm) * sm_count();
   const unsigned grid = static_cast<unsigned>(geo.n_tiles < most ? geo.n_tiles : most);
+  const size_t tiles = (geo.n_tiles + grid - 1) / grid;  // of a CTA
+  geo.stages = static_cast<int>(min(min(fit, tiles), static_cast<size_t>(kMaxStages)));
   const size_t smem = w + stage * geo.stages;
   return a.in_fmt == LC_FMT_F32 ? launch_norm_v<true>(v, a, geo, grid, smem, st) : launch_norm_v<false>(v, a, geo, grid, smem, st);
 }
