@@ -558,7 +558,8 @@ typedef struct lc_kv8_cache {
  * holds tokens (of a position below pos0[s]) takes the larger of its scale and 2^e; when its
  * scale grows, its older codes are rounded again to the new one (to nearest, ties to even).
  * Infinities become +-448 2^e, NaN the E4M3 NaN.  Rows of a block past the newest token are
- * left as they were.  A block that is written must belong to one sequence alone. */
+ * left as they were.  A sequence with pos0 < 0 is skipped.  A block that is written must belong
+ * to one sequence alone. */
 typedef struct lc_kv8_append_args {
   lc_kv8_cache cache;
   int32_t num_seqs;

@@ -241,6 +241,24 @@ def test_w4_extreme_rows_stay_apart():
     assert ok.all()
 
 
+@pytest.mark.parametrize("n", [1, 20, 40])
+def test_w4_scales_at_the_ends_of_e8m0(n):
+    """Weight scales 2^-127 .. 2^127 against x scales that bring the products back; the sums as in
+    test_w4.  x at 2^-127 of a block's scale next to weights at 2^127."""
+    r = rng_for(31, n)
+    K, dg = 224, 40
+    codes, _ = make_w4(r, 1, dg, K)
+    we = np.repeat(np.array([[-127, 127, -126, 126, 0, 100, -100]]), dg, 0)  # per block of 32, the same in every row
+    scales = (we + 127).astype(np.uint8)[None]
+    xc = r.integers(0, 256, (n, K), dtype=np.uint8)
+    xc = np.where((xc & 0x7f) == 0x7f, xc ^ 1, xc).astype(np.uint8)
+    xs = np.repeat((127 - we[:1]).astype(np.uint8), n, 0)
+    x64 = R.mxfp8_rows(xc, xs)
+    ref, mag, _ = w4_reference(x64, codes, scales, 1, K, dg)
+    got = run_w4(torch.from_numpy(xc).cuda(), torch.from_numpy(xs).cuda(), codes, scales, 1, K, dg, F32)
+    assert np.all(np.abs(got - ref) <= K * 2.0 ** -24 * mag + 2.0 ** -24 * np.abs(ref) + 1e-30)
+
+
 def test_w4_reads_what_the_quantiser_writes():
     r = rng_for(9)
     K, dg, n = 256, 96, 4

@@ -302,3 +302,46 @@ def test_prefill_with_few_rows_splits_the_keys(g, D, nq, kv, W):
     got = run_attn(GpuCache(c), q, st, lens - n, lens, g, False, W=W, sink=sink)
     assert got[2] == 0
     check_attn(c, np64(q), st, lens - n, lens, g, got[0], got[1], W=W, sink=sink)
+
+
+def test_calls_between_other_kernels_without_waiting():
+    """The kernels start before the one in front of them ends: chains with torch's kernels in front, between
+    and behind, sent without a pause, give what the same chain gives with a pause after every call."""
+    r = rng_for(14)
+    n, d, dg = 9, 512, 384
+    codes, scales = make_w4(r, 1, dg, d)
+    ct, st = torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()
+    S, H, Hkv, D, bt = n, 6, 3, 64, 16
+    start = np.arange(S + 1)
+
+    def chain(pause):
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        c = make_cache(rng_for(15), [600] * S, Hkv, D, bt)
+        gc = GpuCache(c)
+        x, y8, ys = (torch.empty(n, d, device="cuda"), torch.empty(n, d, dtype=torch.uint8, device="cuda"),
+                     torch.empty(n, d // 32, dtype=torch.uint8, device="cuda"))
+        y = torch.empty(n, dg, device="cuda", dtype=torch.bfloat16)
+        kv, pos = i32(np.full(S, 301)), i32(np.full(S, 300))
+        q0 = gpu(np.zeros((S, H, D)), BF16)
+        a, out, lse, status, keep = attn_args(gc, q0, start, np.full(S, 300), np.full(S, 301), H, True, max_kv=600)
+        a.q, a.q_pos0, a.kv_len = p(y), p(pos), p(kv)
+        ap = lc.Kv8AppendArgs(cache=gc.args, num_seqs=S, in_fmt=BF16, max_tok=1, k=p(y), v=p(y), k_stride=dg, v_stride=dg, tok_start=p(keep[0]), pos0=p(pos))
+        got = []
+        for _ in range(40):
+            for f in (lambda: x.normal_(generator=gen),
+                      lambda: lc.lc_add_rms_norm(lc.AddRmsNormArgs(n_rows=n, d=d, in_fmt=F32, x=p(x), out_fmt=MXFP8, y=p(y8), y_scale=p(ys), eps=1e-6)),
+                      lambda: lc.lc_w4_proj(lc.W4ProjArgs(n_q=n, G=1, K=d, d_g=dg, in_fmt=MXFP8, out_fmt=BF16, x=p(y8), x_scale=p(ys), w=p(ct), w_scale=p(st), y=p(y))),
+                      lambda: y.mul_(0.125),
+                      lambda: lc.lc_kv8_append(ap),
+                      lambda: lc.lc_kv8_attn_decode(a),
+                      lambda: pos.add_(1), lambda: kv.add_(1),
+                      lambda: got.append((out.clone(), lse.clone(), y8.clone()))):
+                f()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got, [t.clone() for t in gc.t]
+    (a, ca), (b, cb) = chain(False), chain(True)
+    for u, v in zip(a, b):
+        assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(u, v))
+    assert all(torch.equal(s, t) for s, t in zip(ca, cb))
