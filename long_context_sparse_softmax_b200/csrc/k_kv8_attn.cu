@@ -20,9 +20,10 @@
 // Warps of a CTA take 16-key steps in turn and join through shared memory; the keys of a row
 // tile are split over CTAs, joined by k_kv8_combine.
 //
-// HBM bounds it: a step of a warp is 4 KB (128 dims), the next one travels meanwhile.  One context of
-// 262144 tokens, 8 shared heads, 64 queries' heads: 97 us, 5.5 TB/s (85 % of the measured copy rate; the
-// join is 9 us of it).  32 contexts up to 16384: 122 us, 4.5 TB/s: here a CTA has 16 steps a warp, and its
+// HBM bounds it: a step of a warp is 4 KB (128 dims), the next one travels meanwhile and
+// the one after is on its way to L2.  One context of 262144 tokens, 8 shared heads, 64 queries' heads:
+// 94 us, 5.7 TB/s (88 % of the measured copy rate; the join is 9 us of it).  32 contexts up to 16384:
+// 119.5 us, 4.6 TB/s: here a CTA has 16 steps a warp, and its
 // start (block ids, then keys), its end and the join cost as much as 200 keys.  What brought it there:
 // two conversions per instruction pair and no divisions by the block size (209 -> 157 us for the batch),
 // block ids before the queries, 32-bit index arithmetic (143), splits of 1024 keys (127); splits that
@@ -210,6 +211,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     }
   };
 
+  // A step's lines into L2, 128 bytes of keys or values a lane: asked for one turn ahead of load(), where
+  // registers for a second step in flight would cost a CTA of the multiprocessor (batch 123 -> 119.5 us,
+  // one long context 97.5 -> 94.2; two turns ahead 120.2 and 95.1, four 124.6 and 100).
+  auto prefetch = [&](int t0) {
+    constexpr int kLines = 16 * D / 128;
+    static_assert(2 * kLines <= 32);
+    const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
+    if (pg < 0) return;
+    const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
+    if (lane < 2 * kLines) asm volatile("prefetch.global.L2 [%0];\n" ::"l"((lane < kLines ? c.k : c.v) + at + lane % kLines * 128));
+  };
   auto step = [&](int t0, Step<D>& cur) {
     const int ip = (t0 >> bt_log) - pg0;
     if (s_page[ip] >= 0) {
@@ -366,9 +378,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   while (c0 < c1) {
     for (int t0 = c0 + warp * 16; t0 < c1; t0 += 2 * kTurn) {
       load(t0 + kTurn, odd);
+      prefetch(t0 + 2 * kTurn);
       step(t0, even);
       if (t0 + kTurn >= c1) break;
       load(t0 + 2 * kTurn, even);
+      prefetch(t0 + 3 * kTurn);
       step(t0 + kTurn, odd);
     }
     c0 += kChunk;
