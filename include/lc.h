@@ -541,7 +541,7 @@ typedef struct lc_kv8_cache {
   int32_t D;               /* dims per head: 64 or 128 */
   int32_t bt;              /* tokens per block: 16, 32, 64 or 128 */
   int32_t n_blocks;        /* blocks in the arrays */
-  int32_t table_cols;      /* columns of table */
+  int32_t table_cols;      /* columns of table: at most 2^30 tokens */
   int32_t reserved;
   uint8_t* k;              /* [n_blocks, H_kv, bt, D] E4M3 */
   uint8_t* v;              /* [n_blocks, H_kv, bt, D] E4M3 */

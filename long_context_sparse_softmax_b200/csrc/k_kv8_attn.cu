@@ -579,8 +579,10 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
   geo.rows = geo.tc ? kv8_tc_rows(a.cache.D) : geo.g <= 8 ? 8 : 16;
   geo.row_tiles = static_cast<int>((all + geo.rows - 1) / geo.rows);
   geo.n_split = 1;
-  int n = a.max_kv;
-  if (a.W > 0 && a.W + a.max_q - 1 < n - 16) n = a.W + a.max_q - 1 + 16;
+  // keys of a row tile: as the kernels cut them, and of the window with its start rounded down
+  int64_t keys = min(a.max_kv, a.cache.table_cols * a.cache.bt);
+  if (a.W > 0) keys = min(keys, static_cast<int64_t>(a.W) + a.max_q - 1 + 16);
+  const int n = static_cast<int>(keys);
   if (geo.tc) {
     // fewer CTAs than the device holds at once: split the keys, at least 4 tiles of 128 each
     const int64_t ctas = static_cast<int64_t>(geo.row_tiles) * a.cache.H_kv * a.num_seqs;

@@ -194,8 +194,8 @@ lc_status w4_proj(const lc_w4_proj_args* a, void* stream) {
 lc_status check_kv8(const lc_kv8_cache& c, bool need) {
   if (c.H_kv < 1 || c.n_blocks < 0 || c.table_cols < 0) return LC_ERR_ARG;
   if ((c.D != 64 && c.D != 128) || (c.bt != 16 && c.bt != 32 && c.bt != 64 && c.bt != 128)) return LC_ERR_UNSUPPORTED;
-  // token positions are 32-bit
-  if (static_cast<int64_t>(c.table_cols) * c.bt > INT32_MAX) return LC_ERR_ARG;
+  // a sequence's tokens are 32-bit, and the kernels' steps past its end must be as well
+  if (static_cast<int64_t>(c.table_cols) * c.bt > 1 << 30) return LC_ERR_ARG;
   if (static_cast<int64_t>(c.n_blocks) * c.H_kv > INT32_MAX) return LC_ERR_ARG;  // so are block slots
   if (!need) return LC_OK;
   if (!c.k || !c.v || !c.k_scale || !c.v_scale || !c.table) return LC_ERR_ARG;

@@ -31,7 +31,7 @@ struct Kv8Range {
 __device__ __forceinline__ Kv8Range kv8_range(int kv, int W, int p_first, int p_last) {
   Kv8Range r;
   r.hi = p_last < kv - 1 ? p_last + 1 : kv;
-  r.lo = W > 0 ? max(0, p_first - (W - 1)) : 0;
+  r.lo = W > 0 && p_first >= W ? p_first - (W - 1) : 0;  // W up to the type's last value
   r.lo16 = r.lo & ~15;
   if (r.hi <= r.lo) r.hi = r.lo16;
   return r;

@@ -131,3 +131,24 @@ def test_workspace_covers_every_shorter_sequence():
         for n in [*range(1, 12000, 61), *range(12000, 1500000, 9973)]:
             assert need(n) >= most
             most = need(n)
+
+
+@pytest.mark.parametrize("which", ["prefill", "decode"])
+def test_a_window_wider_than_the_context_needs_the_same_workspace(which):
+    """A window up to the type's last value is no window: no sum with it may pass 32 bits."""
+    d = which == "decode"
+    for max_q in (1,) if d else (1, 2, 3, 4000):
+        def need(W, max_kv=60000):
+            return lc.lc_kv8_attn_workspace_bytes(lc.Kv8AttnArgs(
+                cache=cache(table_cols=1024), H=8, num_seqs=1, n_q=max_q, max_q=max_q, max_kv=max_kv, W=W), d)
+        for W in (60000, (1 << 31) - max_q, (1 << 31) - 17, (1 << 31) - 16, (1 << 31) - 1):
+            assert need(W) == need(0)
+        # no more keys than the table has columns for: 65536
+        assert need(0, (1 << 31) - 1) == need(0, 65536)
+
+
+def test_cache_of_at_most_2_30_tokens():
+    for bt in (16, 32, 64, 128):
+        assert append(cache(table_cols=(1 << 30) // bt, bt=bt), num_seqs=0) == OK
+        assert append(cache(table_cols=(1 << 30) // bt + 1, bt=bt), num_seqs=0) == ARG
+        assert attn("prefill", cache=cache(table_cols=(1 << 30) // bt + 1, bt=bt)) == ARG

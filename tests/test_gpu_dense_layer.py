@@ -608,3 +608,17 @@ def test_attn_is_independent_of_the_batch():
         one = R.Cache(c.k, c.ks, c.v, c.vs, c.table[s:s + 1])
         b = run_attn(GpuCache(one), q[s:s + 1], [0, 1], kv[s:s + 1] - 1, kv[s:s + 1], H, True)
         assert np.array_equal(a[0][s], b[0][0]) and np.array_equal(a[1][s], b[1][0])
+
+
+@pytest.mark.parametrize("decode,nq", [(True, 1), (False, 2), (False, 40)])
+def test_attn_window_of_the_types_last_value(decode, nq):
+    """Wider than any context: the same answer as without a window, bit by bit."""
+    r = rng_for(decode, nq, 99)
+    kv = np.array([2600])
+    c = make_cache(r, kv, 1, 64, 64)
+    q = gpu(r.standard_normal((nq, 4, 64)) * 2.0 ** -8, BF16)
+    want = run_attn(GpuCache(c), q, [0, nq], kv - nq, kv, 4, decode)
+    check_attn(c, np64(q), np.array([0, nq]), kv - nq, kv, 4, want[0], want[1])
+    for W in (2600, (1 << 31) - nq, (1 << 31) - 1):
+        got = run_attn(GpuCache(c), q, [0, nq], kv - nq, kv, 4, decode, W=W)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == 0
