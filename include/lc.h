@@ -510,7 +510,8 @@ lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);
  * BF16 row is split there into two E4M3 terms, exact for values down to 2^-15 of the largest
  * of their 32-value block and within 2^-22 of that largest value below.  A NaN or an infinity
  * in a BF16 row makes the row's outputs of that group NaN.  Each 32 rows of BF16 x (64 of
- * MXFP8) read the weights once: for many rows use a 16-bit product instead.
+ * MXFP8) read the weights once: for many rows use a 16-bit product instead.  Up to 65535 times
+ * as many rows; G K up to 2^30; fewer than 2^24 tiles of 128 outputs.
  * ------------------------------------------------------------------------------- */
 typedef struct lc_w4_proj_args {
   int32_t n_q;             /* rows of x */

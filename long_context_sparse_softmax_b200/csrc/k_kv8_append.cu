@@ -162,8 +162,8 @@ cudaError_t launch_kv8_append(const lc_kv8_append_args& a, cudaStream_t st) {
   // max_tok tokens touch at most 1 + (max_tok - 1 + bt - 1) / bt blocks, wherever the first lies
   const int bt = a.cache.bt;
   const int64_t max_blk = 1 + (static_cast<int64_t>(a.max_tok) + bt - 2) / bt;
+  if (2.0 * max_blk * a.num_seqs * a.cache.H_kv > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int64_t grid = max_blk * 2 * a.num_seqs * a.cache.H_kv;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   if (a.in_fmt == LC_FMT_F32) return launch<true>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
   return launch<false>(a, static_cast<unsigned>(grid), static_cast<uint32_t>(max_blk), st);
 }

@@ -598,8 +598,8 @@ size_t align16(size_t n) { return (n + 15) & ~size_t{15}; }
 
 template <int D>
 cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t st) {
+  if (1.0 * geo.n_split * geo.row_tiles * a.cache.H_kv * a.num_seqs > INT32_MAX) return cudaErrorInvalidConfiguration;
   const int64_t grid = static_cast<int64_t>(geo.n_split) * geo.row_tiles * a.cache.H_kv * a.num_seqs;
-  if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
   const size_t rows = static_cast<size_t>(a.n_q) * a.H;
   float* ws_o = static_cast<float*>(a.workspace);
   float2* ws_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align16(rows * geo.n_split * D * 4));

@@ -178,10 +178,9 @@ lc_status w4_proj(const lc_w4_proj_args* a, void* stream) {
   if (a->out_fmt != LC_FMT_F32 && a->out_fmt != LC_FMT_BF16) return LC_ERR_ARG;
   const bool mx = a->in_fmt == LC_FMT_MXFP8;
   if (!mx && a->in_fmt != LC_FMT_BF16) return LC_ERR_ARG;
-  // launch limits: 2^31 - 1 CTAs in x, 65535 in y
+  // launch limits: 2^31 - 1 CTAs in x (8 or fewer a tile), 65535 in y (64 rows each, 32 of BF16)
   const int64_t tiles = static_cast<int64_t>(a->G) * ((static_cast<int64_t>(a->d_g) + 127) / 128);
-  if (tiles > (int64_t{1} << 24) || static_cast<int64_t>(a->G) * a->K > (int64_t{1} << 30) ||
-      (static_cast<int64_t>(a->n_q) + 63) / 64 > 65535)
+  if (tiles >= (int64_t{1} << 24) || static_cast<int64_t>(a->G) * a->K > (int64_t{1} << 30) || a->n_q > 65535 * (mx ? 64 : 32))
     return LC_ERR_UNSUPPORTED;
   if (a->n_q == 0) return LC_OK;
   if (!a->x || !a->w || !a->w_scale || !a->y || (mx && !a->x_scale)) return LC_ERR_ARG;

@@ -152,3 +152,8 @@ def test_cache_of_at_most_2_30_tokens():
         assert append(cache(table_cols=(1 << 30) // bt, bt=bt), num_seqs=0) == OK
         assert append(cache(table_cols=(1 << 30) // bt + 1, bt=bt), num_seqs=0) == ARG
         assert attn("prefill", cache=cache(table_cols=(1 << 30) // bt + 1, bt=bt)) == ARG
+
+
+def test_w4_proj_launch_limits():
+    assert w4(n_q=65535 * 32 + 1) == UNSUP and w4(n_q=65535 * 64 + 1, in_fmt=lc.LC_FMT_MXFP8) == UNSUP
+    assert w4(G=1, K=32, d_g=(1 << 31) - 1) == UNSUP and w4(G=1, K=32, d_g=(1 << 31) - 127) == UNSUP
