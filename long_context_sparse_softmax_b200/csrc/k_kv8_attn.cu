@@ -1,14 +1,14 @@
 // kv8_attn: attention over the 8-bit cache (E4M3 codes, one E8M0 scale per block and head).
 //
-// The tokens stream from global memory straight into the registers that the matrix instruction
-// reads; nothing passes through shared memory.  The products are written transposed, keys (then
+// Bulk copies bring 16 keys and their values at a time into a ring of two steps that each warp has for
+// itself; from there they go into the registers that the matrix instruction reads.  The products are written transposed, keys (then
 // dims) on the 16-row side and 8 query rows on the other, so 8 heads that share a cache head fill
 // the instruction:
 //   S^T[16 keys, 8 rows] = K Q^T      (A = K, B = Q),
 //   O^T[16 dims, 8 rows] += V^T P^T   (A = V^T, B = P).
 // The order of the summed dims is free as long as both operands agree, so a thread's A registers
-// of a key are 16 consecutive bytes of its row (four summed dims per step and thread): whole
-// 32-byte sectors, 16-byte loads.  V^T needs two keys' codes of one dim side by side: the thread
+// of a key are D / 4 consecutive bytes of its row (four summed dims per step and thread), read 16 at a
+// time; the copies' swizzle puts what eight lanes read, of keys and of values, into different banks.  V^T needs two keys' codes of one dim side by side: the thread
 // that holds dims 16 g .. 16 g + 15 of keys 2t, 2t + 1 interleaves their bytes (one prmt per four)
 // and widens them.  E4M3 is a subset of F16, so widening is exact.
 //
@@ -20,16 +20,20 @@
 // Warps of a CTA take 16-key steps in turn and join through shared memory; the keys of a row
 // tile are split over CTAs, joined by k_kv8_combine.
 //
-// HBM bounds it: a step of a warp is 4 KB (128 dims), the next one travels meanwhile and
-// the one after is on its way to L2.  One context of 262144 tokens, 8 shared heads, 64 queries' heads:
-// 94 us, 5.7 TB/s (88 % of the measured copy rate; the join is 9 us of it).  32 contexts up to 16384:
-// 119.5 us, 4.6 TB/s: here a CTA has 16 steps a warp, and its
-// start (block ids, then keys), its end and the join cost as much as 200 keys.  What brought it there:
+// HBM bounds it: a step of a warp is 4 KB (128 dims).  One context of 262144 tokens, 8 shared heads, 64
+// queries' heads: 96 us, 5.6 TB/s (86 % of the measured copy rate; the join is 9 us of it).  32 contexts up
+// to 16384: 102 us, 5.4 TB/s (84 %): here a CTA has 16 steps a warp, and what it does besides (about 1100
+// instructions a warp, one after another) costs as much as 100 keys; the join is 6 us.  What brought it there:
 // two conversions per instruction pair and no divisions by the block size (209 -> 157 us for the batch),
-// block ids before the queries, 32-bit index arithmetic (143), splits of 1024 keys (127); splits that
-// fill the device once and a join by a CTA per row (135 -> 100 us for the one).
+// block ids before the queries, 32-bit index arithmetic (143), splits of 1024 keys (127), the ring (119 -> 106:
+// loads of 16 bytes a lane straight into registers kept L1 75 % busy, 99 % for one context; that one lost 94 ->
+// 97), a join without bank conflicts and one pass over a split's block ids (102); splits that fill the device once and a join by a CTA per row
+// (135 -> 100 us for the one).  Three steps in the ring: 109 us and 101; five CTAs a multiprocessor: 114 and 124;
+// three, of a ring of four: 110 and 119; eight, of two warps: 110 and 117; the block ids asked for before the
+// lengths were known, so that a start waits once less: no difference.
 #include "lc_e4m3.cuh"
 #include "lc_kv8.cuh"
+#include "lc_tma.h"
 
 namespace lc {
 
@@ -37,8 +41,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = kKv8MaxSplit;          // keys whose block ids and scales sit in shared memory
-constexpr int kMaxPages = kChunk / 16 + 1;
+constexpr int kMaxPages = kKv8MaxSplit / 16 + 1;  // block ids and scales of a split sit in shared memory
+constexpr long kSpin = 1L << 20;              // a few seconds
 constexpr float kHeadroom = 8.f;              // log2 of the largest weight before R moves
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -54,20 +58,18 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld8(const uint8_t* p) {
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
   return v;
 }
 
-// A 16-key step of one warp.  k: keys g and g + 8, 16 bytes at 16 t (and at 64 + 16 t for 128 dims);
+// A 16-key step of one warp.  k: keys g and g + 8, D / 4 bytes at (D / 4) t;
 // v: keys 2t, 2t + 1, 2t + 8, 2t + 9, D / 8 bytes at (D / 8) g.
 template <int D>
 struct Step {
@@ -77,9 +79,18 @@ struct Step {
 
 }  // namespace
 
+// A warp's steps in flight, in shared memory: its own ring, so that no other warp is waited for.  After
+// the last step the warp's sums lie in the same place.
+template <int D>
+struct Kv8Ring {
+  static constexpr int kStages = 2;
+  static constexpr int kHalf = 16 * D, kStage = 2 * kHalf;  // keys | values
+  static constexpr int kWarp = kStages * kStage, kBytes = kWarps * kWarp + 1024;
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
-    k_kv8_attn(lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
+    k_kv8_attn(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, lc_kv8_attn_args a, Kv8Geom geo, float* __restrict__ ws_o, float2* __restrict__ ws_ml) {
   constexpr int kRows = 8 * NT;
   constexpr int kKS = D / 16;   // summed steps of S
   constexpr int kMT = D / 16;   // 16-dim tiles of O^T
@@ -87,12 +98,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   __shared__ int s_page[kMaxPages];
   __shared__ float s_kf[kMaxPages], s_ev[kMaxPages];
   __shared__ float2 s_ml[kWarps][kRows];
-  __shared__ float s_o[kWarps][kRows][D];
+  using Ring = Kv8Ring<D>;
+  constexpr int kStages = Ring::kStages;
+  __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];
+  extern __shared__ uint8_t smem_raw[];
+  static_assert(kRows * D * 4 <= Ring::kWarp, "the sums' place");
 
   const lc_kv8_cache& c = a.cache;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
   const int bt_log = __ffs(c.bt) - 1;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)) + warp * Ring::kWarp;
+  const uint32_t ring_at = su32(ring), bar_at = su32(s_bar[warp]);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(bar_at + 8 * i, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+  }
   pdl_wait();
   pdl_trigger();
   // 32-bit divisions: what a CTA does besides its keys counts when a split has 512 of them
@@ -157,10 +180,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   uint32_t qf[NT][kKS][2];
   float f_row[NT][2];  // rows 2 t4, 2 t4 + 1: log2(e) scale 2^eq
   bool nan_seen = false;  // NaN value codes replaced in an edge step
-  int c0 = k_begin, c1 = min(k_end, c0 + kChunk), pg0 = 0, n_pg = 0;
+  // blocks of [k_begin, k_end): at most kKv8MaxSplit keys (without splits the host saw 256 or fewer)
+  const int pg0 = k_begin >> bt_log, n_pg = k_end > k_begin ? ((k_end - 1) >> bt_log) - pg0 + 1 : 0;
   auto stage_pages = [&]() {
-    pg0 = c0 >> bt_log;
-    n_pg = ((c1 - 1) >> bt_log) - pg0 + 1;
     for (int i = tid; i < n_pg; i += kThreads) {
       int blk = __ldg(c.table + static_cast<int64_t>(s) * c.table_cols + pg0 + i);
       if (blk < 0 || blk >= c.n_blocks) {
@@ -178,49 +200,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       s_ev[i] = blk < 0 ? 0.f : static_cast<float>(kv8_exp(__ldg(c.v_scale + slot)));
     }
   };
-  auto load = [&](int t0, Step<D>& st) {
-    const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
-    if (pg < 0) return;  // never used
-    const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
-    const uint8_t* kp = c.k + at + g8 * D + 16 * t4;
+  // The warp's turns: turn i (key t) uses place i % kStages.  Sent by one lane, a step of a block that is
+  // skipped without copies.
+  int sent = 0, place_in = 0;
+  auto send = [&](int t) {
+    if (t >= k_end) return;
+    if (lane == 0) {
+      const int pg = s_page[(t >> bt_log) - pg0];
+      const uint32_t bar = bar_at + 8 * place_in, dst = ring_at + place_in * Ring::kStage;
+      if (pg < 0) {
+        mbar_arrive(bar);
+      } else {
+        mbar_expect_tx(bar, Ring::kStage);
+        tma_tile3d(dst, &map_k, 0, t & (c.bt - 1), pg * c.H_kv + h, bar);
+        tma_tile3d(dst + Ring::kHalf, &map_v, 0, t & (c.bt - 1), pg * c.H_kv + h, bar);
+      }
+    }
+    ++sent;
+    if (++place_in == kStages) place_in = 0;
+  };
+  // where the swizzled copy put a thread's bytes: 16-byte piece x of row r at piece x ^ r (128 dims), or, with two
+  // rows to 128 bytes, at x ^ (r / 2)
+  const uint32_t at_k = D == 128 ? g8 * 128 + ((2 * t4) ^ g8) * 16 : g8 * 64 + (t4 ^ (g8 >> 1)) * 16;
+  const uint32_t at_v = D == 128 ? t4 * 256 + (g8 ^ (2 * t4)) * 16 : t4 * 128 + ((g8 >> 1) ^ t4) * 16 + (g8 & 1) * 8;
+  auto take = [&](int place, Step<D>& st) {
+    const uint32_t k = ring_at + place * Ring::kStage + at_k, v = ring_at + place * Ring::kStage + Ring::kHalf + at_v;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
-        const uint4 v = ld16(kp + r * 8 * D + x * 64);
-        st.k[r][4 * x] = v.x;
-        st.k[r][4 * x + 1] = v.y;
-        st.k[r][4 * x + 2] = v.z;
-        st.k[r][4 * x + 3] = v.w;
+        const uint4 w = lds16((k + r * 8 * D) ^ (x * 16));
+        st.k[r][4 * x] = w.x;
+        st.k[r][4 * x + 1] = w.y;
+        st.k[r][4 * x + 2] = w.z;
+        st.k[r][4 * x + 3] = w.w;
       }
-    const uint8_t* vp = c.v + at + kVB * g8;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint8_t* p = vp + (2 * t4 + (r & 1) + (r >> 1) * 8) * D;
+      // key 2 t + (r & 1) + 8 (r / 2)
       if constexpr (D == 128) {
-        const uint4 v = ld16(p);
-        st.v[r][0] = v.x;
-        st.v[r][1] = v.y;
-        st.v[r][2] = v.z;
-        st.v[r][3] = v.w;
+        const uint4 w = lds16((v + (r & 1) * 128 + (r >> 1) * 1024) ^ ((r & 1) * 16));
+        st.v[r][0] = w.x;
+        st.v[r][1] = w.y;
+        st.v[r][2] = w.z;
+        st.v[r][3] = w.w;
       } else {
-        const uint2 v = ld8(p);
-        st.v[r][0] = v.x;
-        st.v[r][1] = v.y;
+        const uint2 w = lds8(v + (r & 1) * 64 + (r >> 1) * 512);
+        st.v[r][0] = w.x;
+        st.v[r][1] = w.y;
       }
     }
-  };
-
-  // A step's lines into L2, 128 bytes of keys or values a lane: asked for one turn ahead of load(), where
-  // registers for a second step in flight would cost a CTA of the multiprocessor (batch 123 -> 119.5 us,
-  // one long context 97.5 -> 94.2; two turns ahead 120.2 and 95.1, four 124.6 and 100).
-  auto prefetch = [&](int t0) {
-    constexpr int kLines = 16 * D / 128;
-    static_assert(2 * kLines <= 32);
-    const int pg = t0 < c1 ? s_page[(t0 >> bt_log) - pg0] : -1;
-    if (pg < 0) return;
-    const int64_t at = (((static_cast<int64_t>(pg) * c.H_kv + h) << bt_log) + (t0 & (c.bt - 1))) * D;
-    if (lane < 2 * kLines) asm volatile("prefetch.global.L2 [%0];\n" ::"l"((lane < kLines ? c.k : c.v) + at + lane % kLines * 128));
   };
   auto step = [&](int t0, Step<D>& cur) {
     const int ip = (t0 >> bt_log) - pg0;
@@ -322,12 +351,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 
   // The chain of dependent accesses before the first keys is what a short split waits for: block ids
   // first, then the first keys, and the queries while those travel
-  Step<D> even, odd;
   constexpr int kTurn = 16 * kWarps;  // keys that the warps take in one turn
-  if (c0 < c1) stage_pages();
+  stage_pages();
   __syncthreads();
-  load(c0 + warp * 16, even);
-  if (c0 < c1) stage_scales();
+  for (int i = 0; i < kStages; ++i) send(k_begin + warp * 16 + i * kTurn);
+  stage_scales();
   // queries: B operand, row g8 of each 8-row tile; the row's power of two goes to the logits
   const int64_t q_stride = a.q_stride ? a.q_stride : static_cast<int64_t>(a.H) * D;
 #pragma unroll
@@ -338,13 +366,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     const uint16_t* qr = static_cast<const uint16_t*>(a.q) + (q0 + qi) * q_stride +
                          (static_cast<int64_t>(h) * geo.g + (static_cast<int>(row0) + i * 8 + g8 - qi * geo.g)) * D;
 #pragma unroll
-    for (int k = 0; k < kKS; ++k) {
-      // dims 16 t + 4 (k % 4) .. + 3, past 64 for the second half
-      uint2 v = make_uint2(0, 0);
-      if (on) v = __ldg(reinterpret_cast<const uint2*>(qr + (k / 4) * 64 + 16 * t4 + 4 * (k % 4)));
+    for (int k = 0; k < kKS; k += 2) {
+      // dims (D / 4) t + 4 k .. + 7
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (on) v = __ldg(reinterpret_cast<const uint4*>(qr + (D / 4) * t4 + 4 * k));
       w[k][0] = v.x;
       w[k][1] = v.y;
-      mb = max_u16x2(mb, max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+      w[k + 1][0] = v.z;
+      w[k + 1][1] = v.w;
+      mb = max_u16x2(mb, max_u16x2(max_u16x2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), max_u16x2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
     }
     // the largest magnitude as BF16 bits; only where that is not finite the largest finite one
     mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
@@ -375,28 +405,38 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     f_row[i][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
   }
   __syncthreads();
-  while (c0 < c1) {
-    for (int t0 = c0 + warp * 16; t0 < c1; t0 += 2 * kTurn) {
-      load(t0 + kTurn, odd);
-      prefetch(t0 + 2 * kTurn);
-      step(t0, even);
-      if (t0 + kTurn >= c1) break;
-      load(t0 + 2 * kTurn, even);
-      prefetch(t0 + 3 * kTurn);
-      step(t0 + kTurn, odd);
+  int place = 0;
+  uint32_t parity = 0;
+  bool ok = true;
+  auto arrived = [&](int at, uint32_t par) -> bool {
+    for (long it = 0; it < kSpin; ++it)
+      if (mbar_test(bar_at + 8 * at, par)) return true;
+    set_status(a.status, LC_DEV_TIMEOUT);
+    return false;
+  };
+  for (int t0 = k_begin + warp * 16; t0 < k_end; t0 += kTurn) {
+    ok = __all_sync(0xffffffffu, arrived(place, parity));
+    if (!ok) break;
+    Step<D> cur;
+    take(place, cur);
+    __syncwarp();
+    send(t0 + kStages * kTurn);
+    step(t0, cur);
+    if (++place == kStages) {
+      place = 0;
+      parity ^= 1;
     }
-    c0 += kChunk;
-    c1 = min(k_end, c0 + kChunk);
-    if (c0 >= c1) break;
-    __syncthreads();  // every warp is done with the block ids
-    stage_pages();
-    __syncthreads();
-    load(c0 + warp * 16, even);
-    stage_scales();
-    __syncthreads();
   }
+  // after a wait that ran out: what is still on its way lands (or runs out, too) before the CTA ends
+  if (!ok)
+    for (int i = max(0, sent - kStages); i < sent; ++i)
+      for (long it = 0; it < kSpin && !mbar_test(bar_at + 8 * (i % kStages), (i / kStages) & 1); ++it) {
+      }
+  __syncwarp();
 
-  // join the warps
+  // join the warps.  A pair of dims of a row lies at its index ^ pair_key, so that the 16 lanes of a store, four
+  // rows of the same few dims, meet 16 banks
+  auto pair_key = [](int r, int d) { return D == 128 ? (d >> 5 & 1) | (r & 6) : r >> 1 & 3; };
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -408,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
       if (g8 == 0) s_ml[warp][r] = make_float2(R[i][j], l[i][j]);
 #pragma unroll
       for (int m = 0; m < kMT; ++m)
-        *reinterpret_cast<float2*>(&s_o[warp][r][kVB * g8 + 2 * m]) = make_float2(o[i][m][j], o[i][m][2 + j]);
+        reinterpret_cast<float2*>(ring)[r * (D / 2) + ((kVB / 2 * g8 + m) ^ pair_key(r, kVB * g8))] = make_float2(o[i][m][j], o[i][m][2 + j]);
     }
   const bool nans = __syncthreads_or(nan_seen);
   for (int i = tid; i < n_row * (D / 4); i += kThreads) {
@@ -418,11 +458,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
     for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_ml[w][r].x);
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int key = pair_key(r, d);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float f = ref_factor(s_ml[w][r].x, M);
       L = fmaf(s_ml[w][r].y, f, L);
-      const float4 v = *reinterpret_cast<const float4*>(&s_o[w][r][d]);
+      float4 v = reinterpret_cast<const float4*>(ring + (w - warp) * Ring::kWarp)[r * (D / 4) + (d / 4 ^ key >> 1)];
+      if (key & 1) v = make_float4(v.z, v.w, v.x, v.y);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
@@ -565,8 +607,8 @@ namespace {
 // From this many rows per (sequence, shared head) on, a call takes the tensor-memory kernel: its tiles have
 // 128 rows whether they are full or not, k_kv8_attn reads the keys again for every 8 (or 16) rows.
 // Measured (us, k_kv8_attn / k_kv8_attn_tc), 8 heads of 128 dims, 8 query heads each: one sequence of 8192
-// tokens 17.0 / 17.2 at 16 rows, 20.6 / 19.1 at 32, 34 / 20 at 64; of 65536 60 / 66, 105 / 67, 177 / 68; eight of
-// 8192 37 / 68, 69 / 72, 127 / 74.  8 heads of 64 dims, 4 query heads each, eight of 8192: 44 / 44 at 32, 60 / 46 at 64.
+// tokens 16.5 / 17.3 at 16 rows, 19.9 / 18.1 at 32, 32 / 19 at 64; of 65536 49 / 68, 87 / 66, 161 / 70; eight of
+// 8192 35 / 70, 63 / 71, 116 / 74.  8 heads of 64 dims, 4 query heads each, eight of 8192: 48 / 44 at 32, 66 / 46 at 64.
 constexpr int kTcRows = 32;
 
 // Splits that any row tile of the call can have.
@@ -596,6 +638,21 @@ Kv8Geom geometry(const lc_kv8_attn_args& a, bool decode) {
 
 size_t align16(size_t n) { return (n + 15) & ~size_t{15}; }
 
+template <int D, int NT>
+cudaError_t launch_few(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml, cudaStream_t st) {
+  CUtensorMap map_k = {}, map_v = {};
+  const int64_t slots = static_cast<int64_t>(a.cache.n_blocks) * a.cache.H_kv;
+  if (a.max_kv > 0 && slots > 0) {  // else there is nothing to copy
+    constexpr CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!encode_bytes()) return cudaErrorNotSupported;
+    if (!byte_map3(&map_k, a.cache.k, slots, a.cache.bt, D, 16, swizzle) || !byte_map3(&map_v, a.cache.v, slots, a.cache.bt, D, 16, swizzle))
+      return cudaErrorInvalidValue;
+  }
+  const cudaError_t e = allow_smem<k_kv8_attn<D, NT>>(Kv8Ring<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_kv8_attn<D, NT>, dim3(grid), dim3(kThreads), Kv8Ring<D>::kBytes, st, true, 1, map_k, map_v, a, geo, ws_o, ws_ml);
+}
+
 template <int D>
 cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t st) {
   if (1.0 * geo.n_split * geo.row_tiles * a.cache.H_kv * a.num_seqs > INT32_MAX) return cudaErrorInvalidConfiguration;
@@ -603,11 +660,9 @@ cudaError_t launch(const lc_kv8_attn_args& a, const Kv8Geom& geo, cudaStream_t s
   const size_t rows = static_cast<size_t>(a.n_q) * a.H;
   float* ws_o = static_cast<float*>(a.workspace);
   float2* ws_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + align16(rows * geo.n_split * D * 4));
-  auto go = [&](auto kernel) {
-    return launch_ex(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, st, true, 1, a, geo, ws_o, ws_ml);
-  };
   const cudaError_t e = geo.tc ? launch_kv8_attn_tc(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st)
-                        : geo.rows == 8 ? go(k_kv8_attn<D, 1>) : go(k_kv8_attn<D, 2>);
+                        : geo.rows == 8 ? launch_few<D, 1>(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st)
+                                        : launch_few<D, 2>(a, geo, static_cast<unsigned>(grid), ws_o, ws_ml, st);
   if (e != cudaSuccess || geo.n_split == 1) return e;
   return launch_ex(k_kv8_combine<D>, dim3(static_cast<unsigned>(rows)), dim3(32 * kCombineWarps), 0, st, true, 1, a, geo,
                    static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml));

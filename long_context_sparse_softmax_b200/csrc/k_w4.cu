@@ -37,6 +37,7 @@
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
 #include "lc_ptx.cuh"
+#include "lc_tma.h"
 
 namespace lc {
 
@@ -460,32 +461,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 namespace {
-
-using EncodeBytes = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeBytes encode_bytes() {
-  static EncodeBytes fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeBytes>(nullptr);
-    return reinterpret_cast<EncodeBytes>(f);
-  }();
-  return fn;
-}
-
-// [rows, cols] bytes, row-major, box_cols x box_rows boxes as they lie; what is past either end reads as 0.
-// cols and box_cols are multiples of 16, and so is every column that a copy starts at
-bool byte_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t es[2] = {1, 1};
-  return encode_bytes()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int N, bool kMx>
 cudaError_t launch_w4(const lc_w4_proj_args& a, int split, int tiles_g, cudaStream_t st) {
