@@ -21,13 +21,14 @@
 // tile are split over CTAs, joined by k_kv8_combine.
 //
 // HBM bounds it: a step of a warp is 4 KB (128 dims).  One context of 262144 tokens, 8 shared heads, 64
-// queries' heads: 96 us, 5.6 TB/s (86 % of the measured copy rate; the join is 9 us of it).  32 contexts up
-// to 16384: 102 us, 5.4 TB/s (84 %): here a CTA has 16 steps a warp, and what it does besides (about 1100
-// instructions a warp, one after another) costs as much as 100 keys; the join is 6 us.  What brought it there:
+// queries' heads: 96 us, 5.6 TB/s (86 % of the measured copy rate; the join is 5 us of it).  32 contexts up
+// to 16384: 100 us, 5.5 TB/s (86 %): here a CTA has 16 steps a warp, and what it does besides (about 1100
+// instructions a warp, one after another) costs as much as 100 keys; the join is 5 us.  What brought it there:
 // two conversions per instruction pair and no divisions by the block size (209 -> 157 us for the batch),
 // block ids before the queries, 32-bit index arithmetic (143), splits of 1024 keys (127), the ring (119 -> 106:
 // loads of 16 bytes a lane straight into registers kept L1 75 % busy, 99 % for one context; that one lost 94 ->
-// 97), a join without bank conflicts and one pass over a split's block ids (102); splits that fill the device once and a join by a CTA per row
+// 97), a join without bank conflicts and one pass over a split's block ids (102), two warps a
+// joined row instead of four (100); splits that fill the device once and a join by a CTA per row
 // (135 -> 100 us for the one).  Three steps in the ring: 109 us and 101; five CTAs a multiprocessor: 114 and 124;
 // three, of a ring of four: 110 and 119; eight, of two warps: 110 and 117; the block ids asked for before the
 // lengths were known, so that a start waits once less: no difference.
@@ -501,8 +502,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
 }
 
 // Joins the splits of each row: a CTA per (query, head), its warps take splits in turn (eight at a
-// time in flight) and meet in shared memory.
-constexpr int kCombineWarps = 4;
+// time in flight) and meet in shared memory.  What a warp does besides its splits counts: with two of them the join
+// of 2048 rows of up to 16 splits takes 5 us of a call's 100 (four: 7, eight: 14), of 64 rows of 72 splits 5 of 96
+// (one of 16: 4).
+constexpr int kCombineWarps = 2;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kCombineWarps) k_kv8_combine(lc_kv8_attn_args a, Kv8Geom geo, const float* __restrict__ ws_o,
