@@ -622,3 +622,48 @@ def test_attn_window_of_the_types_last_value(decode, nq):
     for W in (2600, (1 << 31) - nq, (1 << 31) - 1):
         got = run_attn(GpuCache(c), q, [0, nq], kv - nq, kv, 4, decode, W=W)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == 0
+
+
+@pytest.mark.parametrize("D,decode,nq", [(128, True, 1), (128, False, 3), (64, True, 1), (64, False, 3), (128, False, 50), (64, False, 50)])
+def test_attn_cache_that_starts_16_bytes_in(D, decode, nq):
+    """The cache's arrays need 16-byte alignment and no more: the same bits as from an allocation's start."""
+    r = rng_for(D, decode, nq, 16)
+    kv = np.array([1900])
+    c = make_cache(r, kv, 2, D, 32)
+    q = gpu(r.standard_normal((nq, 6, D)) * 2.0 ** -8, BF16)
+    want = run_attn(GpuCache(c), q, [0, nq], kv - nq, kv, 6, decode)
+    check_attn(c, np64(q), np.array([0, nq]), kv - nq, kv, 6, want[0], want[1])
+    gc = GpuCache(c)
+    moved = []
+    for name, i in (("k", 0), ("v", 2)):
+        x = gc.t[i].reshape(-1)
+        y = torch.full((x.numel() + 32,), 0x7f, dtype=torch.uint8, device="cuda")
+        y[16:-16] = x
+        moved.append(y)
+        setattr(gc.args, name, p(y) + 16)
+    got = run_attn(gc, q, [0, nq], kv - nq, kv, 6, decode)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == 0
+
+
+@pytest.mark.parametrize("nq", [1, 2, 24])
+def test_attn_block_slots_past_2_31_bytes(nq):
+    """Blocks whose codes lie past 2^31 and 2^32 bytes of the arrays."""
+    r = rng_for(nq, 31)
+    kv, H, D, bt = np.array([500]), 4, 128, 128
+    c = make_cache(r, kv, 2, D, bt, spare=0)
+    n_blocks = (1 << 32) // (2 * D * bt) + 40
+    small = GpuCache(c)
+    want_q = gpu(r.standard_normal((nq, H, D)) * 2.0 ** -8, BF16)
+    want = run_attn(small, want_q, [0, nq], kv - nq, kv, H, nq == 1)
+    far = np.array([n_blocks - 1, n_blocks // 2 + 3, 7, n_blocks - 33])  # of the sequence's four blocks
+    gc = GpuCache(c)
+    big = []
+    for x, fill in zip(gc.t[:4], (0x7f, 127, 0x7f, 127)):
+        y = torch.full((n_blocks, *x.shape[1:]), fill, dtype=torch.uint8, device="cuda")
+        y[torch.from_numpy(far).cuda()] = x[gc.t[4][0].long()]
+        big.append(y)
+    table = i32(far[None])
+    gc.args = lc.Kv8Cache(H_kv=2, D=D, bt=bt, n_blocks=n_blocks, table_cols=4, k=p(big[0]), v=p(big[2]), k_scale=p(big[1]),
+                          v_scale=p(big[3]), table=p(table))
+    got = run_attn(gc, want_q, [0, nq], kv - nq, kv, H, nq == 1)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == 0
