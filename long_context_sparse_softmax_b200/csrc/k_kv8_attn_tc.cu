@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
   auto pos = [&](int r) { return p0 + static_cast<int>((row0 + r) / geo.g); };
   const Kv8Range rg = kv8_range(kv, a.W, pos(0), pos(n_row - 1));
   const int kb0 = rg.lo16 & ~(kTK - 1);
-  const int all_tiles = rg.hi > kb0 ? (rg.hi - kb0 + kTK - 1) / kTK : 0;
+  const int all_tiles = rg.hi > rg.lo16 ? (rg.hi - kb0 + kTK - 1) / kTK : 0;
   const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * split / geo.n_split);
   const int n_tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (split + 1) / geo.n_split) - tile0;
   const int k0 = kb0 + tile0 * kTK;                      // first key of the CTA
