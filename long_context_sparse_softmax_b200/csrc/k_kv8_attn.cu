@@ -114,8 +114,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3)
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(bar_at + 8 * i, 1);
     fence_mbar_init();
-    prefetch_tensormap(&map_k);
-    prefetch_tensormap(&map_v);
+    if (a.max_kv > 0 && c.n_blocks > 0) {  // else the host made no maps
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_v);
+    }
   }
   pdl_wait();
   pdl_trigger();
@@ -645,7 +647,7 @@ template <int D, int NT>
 cudaError_t launch_few(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml, cudaStream_t st) {
   CUtensorMap map_k = {}, map_v = {};
   const int64_t slots = static_cast<int64_t>(a.cache.n_blocks) * a.cache.H_kv;
-  if (a.max_kv > 0 && slots > 0) {  // else there is nothing to copy
+  if (a.max_kv > 0 && slots > 0) {  // else there is nothing to copy, and the kernel does not touch the maps
     constexpr CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     if (!encode_bytes()) return cudaErrorNotSupported;
     if (!byte_map3(&map_k, a.cache.k, slots, a.cache.bt, D, 16, swizzle) || !byte_map3(&map_v, a.cache.v, slots, a.cache.bt, D, 16, swizzle))

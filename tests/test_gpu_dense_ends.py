@@ -7,7 +7,7 @@ import torch
 
 import long_context_sparse_softmax_b200 as lc
 from tests import dense_ref as R
-from tests.test_gpu_dense_layer import BF16, GpuCache, check_attn, gpu, make_cache, np64, rng_for, run_attn
+from tests.test_gpu_dense_layer import BF16, GpuCache, check_attn, gpu, make_cache, np64, p, rng_for, run_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,31 @@ def test_attn_positions_at_the_types_last_value(nq):
             assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
         else:  # the last positions no longer see the first tokens
             check_attn(c, np64(q), np.array([0, nq]), np.array([far]), kv, 4, got[0], got[1], W=W)
+
+
+# ------------------------------------------------------------------ caches that hold nothing
+@pytest.mark.parametrize("nq", [1, 3, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_without_a_cache(D, nq):
+    """max_kv 0 with no arrays behind the cache, and a pool of no blocks whose tables name none: every query
+    gets o = 0 and the sink's logit (-inf without one)."""
+    S, H = 3, 6
+    q = gpu(rng_for(D, nq).standard_normal((S * nq, H, D)), BF16)
+    start, pos, kv = np.arange(S + 1) * nq, np.array([0, 5, 100]), np.array([0, 50, 64])
+
+    class Pool:
+        pass
+    none = Pool()
+    none.args = lc.Kv8Cache(H_kv=2, D=D, bt=16, n_blocks=0, table_cols=0)
+    empty = Pool()
+    table = torch.full((S, 4), -1, dtype=torch.int32, device="cuda")
+    table[1, 0], table[2, 3] = 0, 7  # outside a pool of no blocks
+    room = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    empty.args = lc.Kv8Cache(H_kv=2, D=D, bt=16, n_blocks=0, table_cols=4, k=p(room), v=p(room), k_scale=p(room), v_scale=p(room), table=p(table))
+    for sink in (None, np.float32([-3, 0, 1, 2, 90, -np.inf])):
+        for decode in ([True, False] if nq == 1 else [False]):
+            for pool, max_kv, status in ((none, 0, 0), (empty, 0, 0), (empty, 64, lc.LC_DEV_BAD_BLOCK)):
+                got = run_attn(pool, q, start, pos, kv, H, decode, sink=sink, max_kv=max_kv)
+                assert got[2] == status
+                assert not got[0].any()
+                assert np.array_equal(got[1], np.broadcast_to(-np.inf if sink is None else sink.astype(np.float64), (S * nq, H)))
