@@ -507,11 +507,11 @@ lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);
  *   y[n, g d_g + c] = sum_k x[n, g K + k] W_g[c, k],  0 <= c < d_g,
  * W in MXFP4 exactly as lc_mxfp4_quantize writes its rows.  x is BF16 or MXFP8.  The products
  * run on the block-scaled tensor cores (FP32 accumulation) on the caller's weight bytes; a
- * BF16 row is split there into two E4M3 terms, exact for values down to 2^-15 of the largest
- * of their 32-value block and within 2^-22 of that largest value below.  A NaN or an infinity
- * in a BF16 row makes the row's outputs of that group NaN.  Each 32 rows of BF16 x (64 of
- * MXFP8) read the weights once: for many rows use a 16-bit product instead.  Up to 65535 times
- * as many rows; G K up to 2^30; fewer than 2^24 tiles of 128 outputs.
+ * BF16 row is split there into two E4M3 terms, exact for values of at least 1 / 14336 (2^-13.8)
+ * of the largest of their 32-value block and within 2^-21.8 of that largest value below.  A NaN
+ * or an infinity in a BF16 row makes the row's outputs of that group NaN.  Each 32 rows of BF16
+ * x (64 of MXFP8) read the weights once: for many rows use a 16-bit product instead.  Up to 65535
+ * times as many rows; G K up to 2^30; fewer than 2^24 tiles of 128 outputs.
  * ------------------------------------------------------------------------------- */
 typedef struct lc_w4_proj_args {
   int32_t n_q;             /* rows of x */

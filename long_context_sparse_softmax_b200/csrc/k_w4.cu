@@ -7,7 +7,9 @@
 // E4M3 with their E8M0 scales, and accumulates in FP32 in tensor memory.  A BF16 row becomes two
 // columns of B: with X the row's scale for a block of 32, hi = e4m3(x / X) and lo = e4m3(16 (x / X
 // - hi)) at the scale X / 16.  An E4M3 value keeps 4 significant bits, the rest of a BF16 value
-// fits the other 4: hi + lo is x exactly down to 2^-15 of the block's largest value.
+// fits the other 4.  The block's largest value is above 224 X and lo's step is 2^-13 X: hi + lo is x
+// exactly from 2^-6 X on, that is from 1 / 14336 of the largest value (2^-13.8) on, and within 2^-14 X,
+// 2^-21.8 of the largest value, below.
 //
 // A CTA holds one tile of 128 outputs of a group and a range of its inputs, in steps of 128:
 //   * warps 24 and 25: one thread each copies codes (pairs of steps: 128 bytes of a row) and x into
@@ -25,14 +27,16 @@
 // What bounds it is the chain through these roles, not memory: one row through 7168 x 4096 takes
 // 9.1 us in a graph (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.5 us for 14
 // steps (scales -> MMAs -> stage free), 1.4 us to join 4 CTAs, the rest is the start of the next
-// cluster.  32 rows through 8 groups of 4096 x 1024: 15.3 us, of which widening x (16 conversions per
-// 8 values, in every CTA that shares them) takes 850 cycles a step; 17 rows of MXFP8 through
+// cluster.  32 rows through 8 groups of 4096 x 1024: 14.9 us, of which widening x (16 conversions per
+// 8 values, in every CTA that shares them) took 850 cycles a step when the whole took 15.3; 17 rows of MXFP8 through
 // 7168 x 7000: 14.3 us.
 // Tried: cp.async in place of the bulk copies (50 cycles of issue each: 12.7 and 18.4 us), one x
 // block per thread (1000 cycles a step), two steps per round of the issuing warps (11.0 and 16.7, when
 // this took 10.7 and 16.4), BF16 weights by table lookup for the warps' own matrix instruction (9.5 us
 // for one row, then 10.7 here, and 18.4: bound by the integer pipe).
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
@@ -300,57 +304,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&xfull[slot], (i / L::kRawX) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
       const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
       const bool in = (s_begin + i) * 4 + xb < a.K / 32;  // else the next group's values
+      // Lays out the rows; a block whose largest value is near BF16's end, or not finite, once more with `end`
+      // (what can go wrong there is looked at in that pass alone: in the other it cost 0.2 us of 15)
+      auto lay_out = [&](auto pass) -> bool {
+        constexpr bool end = pass.value;
+        bool again = false;
 #pragma unroll
-      for (int m = 0; m < kU; ++m) {
-        const int t = t0 + kXTok * m;
-        if (t - (lane / kLpr) >= n_tok) break;  // the same for every lane
-        uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * (kXT * 16));
-        if (!in) v = make_uint4(0, 0, 0, 0);
-        if constexpr (kMx) {
-          if (t >= n_tok) continue;
-          st_shared16(Bt + sw128_off(t, xc), v);
-          if (scaler) st_shared1(sf + sf_off(t, xb), sc[m]);
-        } else {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          // the block's largest magnitude as BF16 bits (an infinity's or a NaN's are larger still)
-          uint32_t mb = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-          mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-          mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-          mb = max(mb & 0xffffu, mb >> 16);
-          bool inf = false;
-          if (__any_sync(0xffffffffu, mb >= 0x7f80u)) {  // the largest finite value, then
-            float amax = 0.f;
-            for (int j = 0; j < 4; ++j) {
-              amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[j] << 16)), finite_abs(__uint_as_float(w[j] & 0xffff0000u))));
-              inf |= ((w[j] & 0x7f80u) == 0x7f80u) | ((w[j] & 0x7f800000u) == 0x7f800000u);
+        for (int m = 0; m < kU; ++m) {
+          const int t = t0 + kXTok * m;
+          if (t - (lane / kLpr) >= n_tok) break;  // the same for every lane
+          uint4 v = ld_shared16(raw + slot * L::kRawXBytes + m * (kXT * 16));
+          if (!in) v = make_uint4(0, 0, 0, 0);
+          if constexpr (kMx) {
+            if (t >= n_tok) continue;
+            st_shared16(Bt + sw128_off(t, xc), v);
+            if (scaler) st_shared1(sf + sf_off(t, xb), sc[m]);
+          } else {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            // the block's largest magnitude as BF16 bits (an infinity's or a NaN's are larger still)
+            uint32_t mb = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+            mb = max_u16x2(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+            mb = max(mb & 0xffffu, mb >> 16);
+            again |= mb >= 0x7f78u;  // 248 2^120
+            bool inf = false;
+            if constexpr (end) {  // the largest finite value
+              float amax = 0.f;
+              for (int j = 0; j < 4; ++j) {
+                amax = fmaxf(amax, fmaxf(finite_abs(__uint_as_float(w[j] << 16)), finite_abs(__uint_as_float(w[j] & 0xffff0000u))));
+                inf |= ((w[j] & 0x7f80u) == 0x7f80u) | ((w[j] & 0x7f800000u) == 0x7f800000u);
+              }
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+              mb = __float_as_uint(amax) >> 16;
             }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            mb = __float_as_uint(amax) >> 16;
-          }
-          // 16 / X's exponent has to fit E8M0 too, and 2^-e FP32
-          const int e = mb > 0 ? min(max(e4m3_scale_exp(__uint_as_float(mb << 16)), -120), 119) : 0;
-          const float f = pow2f(-e);
-          uint16_t h8[4], l8[4];
+            // from -123, where X / 16 is the least E8M0 value (BF16's subnormals are exact from there), to 120, the
+            // exponent of the largest BF16 value
+            const int e = mb > 0 ? max(e4m3_scale_exp(__uint_as_float(mb << 16)), -123) : 0;
+            const float f = pow2f(-e);
+            // 248 X and more would round up to 256 X, which is 2^128 under the largest X: there hi takes 240 X and lo
+            // the rest (8 X .. 15 X, exact), so that no term passes FP32's range by itself
+            const __half2 most = __float2half2_rn(e > 119 ? 240.f : 448.f);
+            uint16_t h8[4], l8[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // x / X in F16: exact, or below 2^-17, where both terms are 0 anyway
-            const __half2 y = __floats2half2_rn(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
-            h8[j] = f16x2_to_e4m3x2(y);
-            l8[j] = f16x2_to_e4m3x2(__hmul2(__hsub2(y, e4m3x2_to_f16x2(h8[j])), __float2half2_rn(16.f)));  // exact before the rounding
-          }
-          if (t >= n_tok) continue;
-          uint32_t h0 = h8[0] | static_cast<uint32_t>(h8[1]) << 16;
-          if (inf) h0 |= 0x7fu;  // an infinity has no E4M3 code; like a NaN it makes the outputs NaN
-          const uint32_t off = sw128_off(t, xc >> 1) + (xc & 1) * 8;
-          st_shared8(Bt + off, h0, h8[2] | static_cast<uint32_t>(h8[3]) << 16);
-          st_shared8(Bt + off + kTok * 128, l8[0] | static_cast<uint32_t>(l8[1]) << 16, l8[2] | static_cast<uint32_t>(l8[3]) << 16);
-          if (scaler) {
-            st_shared1(sf + sf_off(t, xb), e + 127);
-            st_shared1(sf + sf_off(kTok + t, xb), e - 4 + 127);
+            for (int j = 0; j < 4; ++j) {
+              // x / X in F16: exact, or below 2^-17, where both terms are 0 anyway
+              const __half2 y = __floats2half2_rn(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+              h8[j] = f16x2_to_e4m3x2(end ? __hmin2_nan(__hmax2_nan(y, __hneg2(most)), most) : y);
+              l8[j] = f16x2_to_e4m3x2(__hmul2(__hsub2(y, e4m3x2_to_f16x2(h8[j])), __float2half2_rn(16.f)));  // exact before the rounding
+            }
+            if (t >= n_tok) continue;
+            uint32_t h0 = h8[0] | static_cast<uint32_t>(h8[1]) << 16;
+            if (inf) h0 |= 0x7fu;  // an infinity has no E4M3 code; like a NaN it makes the outputs NaN
+            const uint32_t off = sw128_off(t, xc >> 1) + (xc & 1) * 8;
+            st_shared8(Bt + off, h0, h8[2] | static_cast<uint32_t>(h8[3]) << 16);
+            st_shared8(Bt + off + kTok * 128, l8[0] | static_cast<uint32_t>(l8[1]) << 16, l8[2] | static_cast<uint32_t>(l8[3]) << 16);
+            if (scaler) {
+              st_shared1(sf + sf_off(t, xb), e + 127);
+              st_shared1(sf + sf_off(kTok + t, xb), e - 4 + 127);
+            }
           }
         }
-      }
+        return again;
+      };
+      if (__any_sync(0xffffffffu, lay_out(std::false_type{})) && !kMx) lay_out(std::true_type{});
       mbar_arrive(su32(&xempty[slot]));
       if constexpr (kMx) scale_bytes(i + kTurnsX);
       fence_async_smem();

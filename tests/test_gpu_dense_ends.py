@@ -7,7 +7,8 @@ import torch
 
 import long_context_sparse_softmax_b200 as lc
 from tests import dense_ref as R
-from tests.test_gpu_dense_layer import BF16, GpuCache, check_attn, gpu, make_cache, np64, p, rng_for, run_attn
+from tests.test_gpu_dense_layer import (BF16, F32, GpuCache, check_attn, gpu, make_cache, make_w4, np64, p, rng_for, run_attn, run_w4,
+                                        w4_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,64 @@ def test_attn_without_a_cache(D, nq):
                 assert got[2] == status
                 assert not got[0].any()
                 assert np.array_equal(got[1], np.broadcast_to(-np.inf if sink is None else sink.astype(np.float64), (S * nq, H)))
+
+
+# ---------------------------------------------------------------- the two terms of a BF16 row
+SPLIT = 2.0 ** -14 / 224  # of a block's largest value: half of the second term's step, where that value is 224 X
+
+
+def bf16(bits):
+    """BF16 bit patterns -> float64."""
+    return (np.asarray(bits, np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("n", [1, 8, 20, 40])
+@pytest.mark.parametrize("end", ["largest", "smallest"])
+def test_w4_at_the_ends_of_bf16(n, end):
+    """Rows of the largest finite values (up to 0x7f7f, which needs the scale 2^120) under small weight
+    scales, and rows of subnormal ones under large scales: the bound of every other row, relative to what the
+    row holds.  FP32 sums of K products, the split, the output's rounding."""
+    r = rng_for(n, end == "largest")
+    G, K, dg = 2, 160, 70
+    codes, scales = make_w4(r, G, dg, K)
+    if end == "largest":
+        bits = r.choice([0x7f7f, 0xff7f, 0x7f70, 0xff6f, 0x7f6e, 0x7e80, 0x3f80, 0x0001], (n, G * K))
+        scales = scales - 100
+    else:
+        bits = r.integers(0, 0x0400, (n, G * K)) | r.integers(0, 2, (n, G * K)) << 15  # below 2^-119
+        bits[0, :32] = 1                        # a block of the smallest value there is
+        bits[0, 32:64] = r.integers(0, 128, 32)  # subnormals alone
+        scales = scales + 100
+    x64 = bf16(bits)
+    xt = torch.from_numpy(bits.astype(np.uint16).view(np.int16)).cuda().view(torch.bfloat16)
+    ref, mag, top = w4_reference(x64, codes, scales.astype(np.uint8), G, K, dg)
+    got = run_w4(xt, None, codes, scales.astype(np.uint8), G, K, dg, F32)
+    lim = (K + 1) * 2.0 ** -24 * mag + SPLIT * top
+    assert np.all(np.abs(got - ref) <= lim), np.max(np.abs(got - ref) / lim)
+
+
+@pytest.mark.parametrize("n", [8, 16, 32])
+def test_w4_split_of_every_significand(n):
+    """Against the identity an output is what the two terms make of one value: exact from 1 / 14336 of the
+    block's largest value on, within the bound below.  Every significand as the largest of a block, with 31
+    values of any significand over 24 octaves below it, at exponents whose
+    outputs stay FP32's normal numbers."""
+    r = rng_for(n, 14336)
+    K = 32 * 128
+    x = np.empty((n, 128, 32))
+    for i in range(n):
+        big = bf16(((128 + r.integers(-95, 127, 128)) << 7) | np.arange(128))
+        low = bf16(r.integers(126 << 7, 127 << 7, (128, 31))) * np.exp2(r.integers(-24, 1, (128, 31)).astype(float))  # below 1
+        x[i, :, 0] = big
+        x[i, :, 1:] = big[:, None] * low * r.choice([-1, 1], (128, 31))
+    xt = torch.from_numpy(x.reshape(n, K).astype(np.float32)).cuda().to(torch.bfloat16)
+    x64 = np64(xt)
+    codes = np.zeros((1, K, K // 2), np.uint8)
+    k = np.arange(K)
+    codes[0, k, k // 2] = np.where(k % 2, 0x20, 0x02)  # 1.0
+    got = run_w4(xt, None, codes, np.full((1, K, K // 32), 127, np.uint8), 1, K, K, F32)
+    err = np.abs(got - x64).reshape(n, 128, 32)
+    a = np.abs(x64).reshape(n, 128, 32)
+    top = a.max(2, keepdims=True)
+    assert not err[a * 14336 >= top].any()
+    assert np.all(err <= SPLIT * top), np.max(err / top) * 2.0 ** 21.8
