@@ -301,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int i = first; i < n_step; i += kTurnsX) {
       const int st = i % kStages, slot = i % L::kRawX;
-      if (!wait(&xfull[slot], (i / L::kRawX) & 1) || (i >= kStages && !wait(&empty[st], ((i / kStages) - 1) & 1))) break;
+      // the warp leaves together: its lanes meet in shuffles and votes below
+      const bool ready = wait(&xfull[slot], (i / L::kRawX) & 1) && (i < kStages || wait(&empty[st], ((i / kStages) - 1) & 1));
+      if (!__all_sync(0xffffffffu, ready)) break;
       const uint32_t Bt = su32(Bs) + st * N * kK, sf = su32(SFb) + st * kSf;
       const bool in = (s_begin + i) * 4 + xb < a.K / 32;  // else the next group's values
       // Lays out the rows; a block whose largest value is near BF16's end, or not finite, once more with `end`
@@ -367,7 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return again;
       };
-      if (__any_sync(0xffffffffu, lay_out(std::false_type{})) && !kMx) lay_out(std::true_type{});
+      const bool again = lay_out(std::false_type{});
+      if constexpr (!kMx) {
+        if (__any_sync(0xffffffffu, again)) lay_out(std::true_type{});
+      }
       mbar_arrive(su32(&xempty[slot]));
       if constexpr (kMx) scale_bytes(i + kTurnsX);
       fence_async_smem();
