@@ -386,11 +386,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
           for (int j = 0; j < 32; ++j) ov[j] = 0;
         }
         if (s_nan && store) {
-          // value codes that were replaced: those of the row's keys make its outputs NaN
+          // value codes that were replaced: those of the row's keys make its outputs NaN.  They lie in the
+          // tiles that not every row of the CTA sees whole, below last.lo and from the tile of first.hi on
+          // (elsewhere a NaN has reached O by itself): a few tiles, however long the cache is
           const Kv8Range me = kv8_range(kv, a.W, p, p);
+          const Kv8Range first = kv8_range(kv, a.W, pos(0), pos(0)), last = kv8_range(kv, a.W, pos(n_row - 1), pos(n_row - 1));
+          const int lo = max(me.lo, k0), hi = min(me.hi, k_end);
+          const int below = min(hi, (last.lo + kTK - 1) & ~(kTK - 1)), from = max(lo, first.hi & ~(kTK - 1));
   #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const uint32_t m = kv8_value_nans(c, s, h, max(me.lo, k0), min(me.hi, k_end), d + j);
+            const uint32_t m = kv8_value_nans(c, s, h, lo, below, d + j) | kv8_value_nans(c, s, h, from, hi, d + j);
   #pragma unroll
             for (int b = 0; b < 4; ++b)
               if (m >> (8 * b) & 0xffu) ov[j + b] = 0x7fffffffu;

@@ -7,7 +7,7 @@ import torch
 
 import long_context_sparse_softmax_b200 as lc
 from tests import dense_ref as R
-from tests.test_gpu_dense_layer import (BF16, F32, GpuCache, check_attn, gpu, make_cache, make_w4, np64, p, rng_for, run_attn, run_w4,
+from tests.test_gpu_dense_layer import (BF16, F32, GpuCache, attn_args, check_attn, gpu, make_cache, make_w4, np64, p, rng_for, run_attn, run_w4,
                                         w4_reference)
 
 pytestmark = pytest.mark.gpu
@@ -144,3 +144,83 @@ def test_w4_split_of_every_significand(n):
     top = a.max(2, keepdims=True)
     assert not err[a * 14336 >= top].any()
     assert np.all(err <= SPLIT * top), np.max(err / top) * 2.0 ** 21.8
+
+
+# --------------------------------------------------------------------- NaN among keys and values
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("W", [0, 45])
+@pytest.mark.parametrize("D,bt,g,nq,kv", [
+    (128, 32, 3, 4, 200), (64, 16, 5, 3, 150),      # few rows, one split
+    (128, 64, 3, 9, 3000), (64, 16, 14, 2, 2900),   # few rows, split keys (the second: two row tiles' worth of heads)
+    (128, 32, 4, 70, 900), (64, 64, 3, 100, 700),   # many rows
+    (128, 16, 2, 150, 5000), (64, 128, 7, 40, 4500)])  # many rows behind a long prefix, split keys
+def test_attn_nan_in_every_kind_of_step(D, bt, g, nq, kv, W, where):
+    """A NaN at the last token, among the last queries, right before them, at the start of the first query's
+    window, in front of it (seen by none with a window), in the middle and at token 0: the queries that see
+    it are NaN (from a value: in that dim alone), and the others as without it."""
+    r = rng_for(D, g, nq, W, where == "k")
+    c = make_cache(r, [kv], 1, D, bt)
+    q = gpu(r.standard_normal((nq, g, D)) * 2.0 ** -8, BF16)
+    sees_from = max(0, kv - nq - W + 1) if W else 0
+    for t in sorted({kv - 1, kv - 1 - nq // 2, kv - nq - 1, sees_from, max(sees_from - 1, 0), kv // 2, 0}):
+        bad = R.Cache(c.k.copy(), c.ks, c.v.copy(), c.vs, c.table)
+        dim = int(r.integers(0, D))
+        getattr(bad, where)[c.table[0, t // bt], 0, t % bt, dim] = 0x7f if t % 2 else 0xff
+        got = run_attn(GpuCache(bad), q, [0, nq], [kv - nq], [kv], g, False, W=W)
+        assert got[2] == 0
+        check_attn(bad, np64(q), np.array([0, nq]), [kv - nq], [kv], g, got[0], got[1], W=W)
+        p_ = kv - nq + np.arange(nq)
+        hit = (t <= p_) & ((t > p_ - W) if W else True)
+        nan = np.isnan(got[0])
+        assert nan[hit].all() if where == "k" else (nan[hit][..., dim].all() and nan.sum() == hit.sum() * g)
+        assert not nan[~hit].any()
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("D,bt,g,kv", [(128, 32, 8, 203), (64, 16, 3, 37), (128, 64, 16, 2501)])
+def test_attn_decode_nan_in_the_last_step(D, bt, g, kv, where):
+    """The last 16-key step is partial, and the rows of its block behind the cache are NaN anyway: only a NaN
+    at a token reaches the query, and with a window only one inside it."""
+    r = rng_for(D, g, kv, where == "k")
+    c = make_cache(r, [kv], 2, D, bt)
+    q = gpu(r.standard_normal((1, 2 * g, D)) * 2.0 ** -8, BF16)
+    for t, W in ((kv - 1, 0), (kv & ~15, 0), (kv - 10, 10), (kv - 11, 10), (kv - 10, 9)):
+        bad = R.Cache(c.k.copy(), c.ks, c.v.copy(), c.vs, c.table)
+        getattr(bad, where)[c.table[0, t // bt], 1, t % bt, 5] = 0x7f
+        got = run_attn(GpuCache(bad), q, [0, 1], [kv - 1], [kv], 2 * g, True, W=W)
+        check_attn(bad, np64(q), np.array([0, 1]), [kv - 1], [kv], 2 * g, got[0], got[1], W=W)
+        hit = W == 0 or t > kv - 1 - W
+        nan = np.isnan(got[0])
+        assert nan.sum() == (0 if not hit else g * (D if where == "k" else 1)) and not nan[:, :g].any()
+
+
+def test_attn_nan_behind_a_long_prefix_costs_no_more():
+    """Where a replaced value code is looked for again is the tiles that not every row sees: what a NaN in the
+    last tile costs does not grow with the cache (a scan of all of it would cost 16 times as much here)."""
+    r = rng_for(65536)
+    Hkv, g, D, bt, nq = 8, 8, 64, 64, 640
+
+    def extra(kv):
+        c = make_cache(r, [kv], Hkv, D, bt)
+        q = gpu(r.standard_normal((nq, Hkv * g, D)) * 2.0 ** -8, BF16)
+        gc = GpuCache(c)
+        a, out, lse, status, keep = attn_args(gc, q, [0, nq], [kv - nq], [kv], Hkv * g, False)
+        assert a.workspace_bytes == 0  # the keys are not split
+
+        def took():
+            ms = []
+            for _ in range(5):
+                e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+                e[0].record()
+                lc.lc_kv8_attn_prefill(a)
+                e[1].record()
+                torch.cuda.synchronize()
+                ms.append(e[0].elapsed_time(e[1]))
+            return min(ms)
+        clean = took()
+        gc.t[2][int(c.table[0, (kv - 20) // bt]), :, (kv - 20) % bt, 3] = 0x7f
+        bad = took()
+        nan = torch.isnan(out[-20:, :, 3])
+        assert nan.all() and not torch.isnan(out[-20:, :, :3]).any()
+        return bad - clean
+    assert extra(65536) < 4 * extra(4096)
