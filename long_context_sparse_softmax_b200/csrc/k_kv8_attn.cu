@@ -653,9 +653,8 @@ cudaError_t launch_few(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned g
     if (!byte_map3(&map_k, a.cache.k, slots, a.cache.bt, D, 16, swizzle) || !byte_map3(&map_v, a.cache.v, slots, a.cache.bt, D, 16, swizzle))
       return cudaErrorInvalidValue;
   }
-  const cudaError_t e = allow_smem<k_kv8_attn<D, NT>>(Kv8Ring<D>::kBytes);
-  if (e != cudaSuccess) return e;
-  return launch_ex(k_kv8_attn<D, NT>, dim3(grid), dim3(kThreads), Kv8Ring<D>::kBytes, st, true, 1, map_k, map_v, a, geo, ws_o, ws_ml);
+  constexpr size_t smem = Kv8Ring<D>::kBytes;
+  return launch_big<k_kv8_attn<D, NT>>(smem, dim3(grid), dim3(kThreads), smem, st, 1, map_k, map_v, a, geo, ws_o, ws_ml);
 }
 
 template <int D>

@@ -575,9 +575,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, Shape<D>::kPerSm)
 
 template <int D>
 static cudaError_t launch_d(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml, cudaStream_t st) {
-  const cudaError_t e = allow_smem<k_kv8_attn_tc<D>>(Shape<D>::kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_ex(k_kv8_attn_tc<D>, dim3(grid), dim3(Shape<D>::kThreads), Shape<D>::kSmem, st, true, 1, a, geo, ws_o, ws_ml);
+  constexpr size_t smem = Shape<D>::kSmem;
+  return launch_big<k_kv8_attn_tc<D>>(smem, dim3(grid), dim3(Shape<D>::kThreads), smem, st, 1, a, geo, ws_o, ws_ml);
 }
 
 cudaError_t launch_kv8_attn_tc(const lc_kv8_attn_args& a, const Kv8Geom& geo, unsigned grid, float* ws_o, float2* ws_ml,

@@ -282,11 +282,8 @@ constexpr size_t kRoom = 216 * 1024;  // dynamic shared memory of a multiprocess
 
 template <auto kKernel>
 cudaError_t launch_one(const lc_add_rms_norm_args& a, const NormGeom& geo, unsigned grid, size_t smem, cudaStream_t st) {
-  if (smem > 46 * 1024) {  // 48 KB with the static part need no asking
-    const cudaError_t e = allow_smem<kKernel>(kRoom);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_ex(kKernel, dim3(grid), dim3(kThreads), smem, st, true, 1, a, geo);
+  if (smem > 46 * 1024) return launch_big<kKernel>(kRoom, dim3(grid), dim3(kThreads), smem, st, 1, a, geo);
+  return launch_ex(kKernel, dim3(grid), dim3(kThreads), smem, st, true, 1, a, geo);  // 48 KB with the static part need no asking
 }
 
 template <bool kF32, int kV>

@@ -495,9 +495,7 @@ cudaError_t launch_w4(const lc_w4_proj_args& a, int split, int tiles_g, cudaStre
       !byte_map(&map_x, a.x, a.n_q, static_cast<int64_t>(a.G) * a.K * (kMx ? 1 : 2), kK * (kMx ? 1 : 2), kTok, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(a.G * tiles_g * split), static_cast<unsigned>((a.n_q + kTok - 1) / kTok));
-  const cudaError_t e = allow_smem<k_w4_proj<N, kMx>>(smem);
-  if (e != cudaSuccess) return e;
-  return launch_ex(k_w4_proj<N, kMx>, grid, dim3(kThreads), smem, st, true, split, map_w, map_x, a, split, tiles_g);
+  return launch_big<k_w4_proj<N, kMx>>(smem, grid, dim3(kThreads), smem, st, split, map_w, map_x, a, split, tiles_g);
 }
 
 }  // namespace

@@ -1,5 +1,7 @@
 // C ABI of the CSA / HCA attention library: host-side validation, then one launch (or a
 // short fixed sequence of launches) on the caller's stream.  See include/lc.h.
+#include <cuda.h>
+
 #include <atomic>
 #include <cstdint>
 
@@ -18,6 +20,19 @@ int sm_count() {
     cache[dev].store(n, std::memory_order_relaxed);
   }
   return n;
+}
+
+uint64_t context_id() {
+  using GetId = CUresult (*)(CUcontext, unsigned long long*);
+  static const GetId fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetId", &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      return static_cast<GetId>(nullptr);
+    return reinterpret_cast<GetId>(f);
+  }();
+  unsigned long long id = 0;
+  return fn && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
 }
 
 }  // namespace lc

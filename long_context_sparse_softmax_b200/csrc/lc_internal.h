@@ -41,19 +41,24 @@ cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-// Lets kKernel have `bytes` of dynamic shared memory (the same in every call) on the current device.
-// Asked for once per device: the runtime takes a microsecond each time, a fifth of a short call.
-template <auto kKernel>
-cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
+// Identity of the current context: unique in the process, and another after cudaDeviceReset.  0: none yet.
+uint64_t context_id();
+
+// Launches a kernel that may have `room` bytes of dynamic shared memory (the same in every call; `smem` of
+// them in this one).  The limit belongs to the context and is asked for once in each (the few at once that
+// share a slot take turns): the runtime takes a microsecond each time, a fifth of a short call; the
+// context's identity 0.03 us.
+template <auto kKernel, typename... Args>
+cudaError_t launch_big(size_t room, dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster, const Args&... args) {
+  static std::atomic<uint64_t> asked[16];
+  const uint64_t id = context_id();
+  std::atomic<uint64_t>& slot = asked[id % 16];
+  if (id == 0 || slot.load(std::memory_order_acquire) != id) {
+    const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(room));
+    if (e != cudaSuccess) return e;
+    if (id != 0) slot.store(id, std::memory_order_release);
+  }
+  return launch_ex(kKernel, grid, block, smem, st, true, cluster, args...);
 }
 
 // Streaming multiprocessors of the current device (queried once per device; 148 on B200).
