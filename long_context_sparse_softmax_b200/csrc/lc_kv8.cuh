@@ -25,15 +25,15 @@ __device__ __forceinline__ float ref_factor(float a, float b) { return a == b ? 
 
 // Keys that the rows [row0, row0 + n_row) of one sequence and shared head can see: [lo, hi); row r
 // is query r / g.  lo16 is lo rounded down to 16 (a 16-key step lies in one block).  Positions may be
-// anywhere below 2^31, a window behind the cache or a query before its first token: 0 <= lo16 <= lo <= kv
-// and lo16 <= hi <= kv all the same, so what starts at lo16 neither leaves the table nor 32 bits.
+// anywhere below 2^31, a window behind the cache or a query before its first token: lo16 <= lo <= kv and
+// lo16 <= hi <= kv all the same, so what starts at lo16 neither leaves the table nor 32 bits.
 struct Kv8Range {
   int lo, hi, lo16;
 };
 __device__ __forceinline__ Kv8Range kv8_range(int kv, int W, int p_first, int p_last) {
   Kv8Range r;
-  r.hi = max(min(p_last, max(kv, 0) - 1) + 1, 0);
-  r.lo = min(W > 0 && p_first >= W ? p_first - (W - 1) : 0, r.hi);  // W up to the type's last value
+  r.hi = p_last < kv ? p_last + 1 : kv;
+  r.lo = min(W > 0 && p_first >= W ? p_first - (W - 1) : 0, kv);  // W up to the type's last value
   r.lo16 = r.lo & ~15;
   if (r.hi <= r.lo) r.hi = r.lo16;
   return r;
