@@ -224,3 +224,49 @@ def test_attn_nan_behind_a_long_prefix_costs_no_more():
         assert nan.all() and not torch.isnan(out[-20:, :, :3]).any()
         return bad - clean
     assert extra(65536) < 4 * extra(4096)
+
+
+# ------------------------------------------------------------------------------ many rows
+@pytest.mark.parametrize("mx", [False, True], ids=["bf16", "mxfp8"])
+@pytest.mark.parametrize("n,G,K,dg", [(131, 2, 160, 40), (300, 1, 1056, 300), (1000, 3, 64, 129), (2113, 1, 256, 128)])
+def test_w4_rows_of_a_prompt(n, G, K, dg, mx):
+    """Accepted, if slow: every 32 (64) rows read the weights again.  The bound of test_w4 with the split's own
+    constant."""
+    r = rng_for(n, K, mx)
+    codes, scales = make_w4(r, G, dg, K)
+    x = r.standard_normal((n, G * K)) * np.exp2(r.integers(-12, 13, (n, G * K)))
+    if mx:
+        e = R.scale_exp(R.finite_amax(x.reshape(n, -1, 32), 2), -127, 127, 0)
+        xc = R.e4m3_codes(x * np.repeat(np.exp2(-e.astype(float)), 32, 1))
+        sc = (e + 127).astype(np.uint8)
+        x64, xt, xs = R.mxfp8_rows(xc, sc), torch.from_numpy(xc).cuda(), torch.from_numpy(sc).cuda()
+    else:
+        xt, xs = gpu(x, BF16), None
+        x64 = np64(xt)
+    ref, mag, top = w4_reference(x64, codes, scales, G, K, dg)
+    got = run_w4(xt, xs, codes, scales, G, K, dg, F32)
+    lim = (K + 1) * 2.0 ** -24 * mag + (0 if mx else SPLIT * top)
+    assert np.all(np.abs(got - ref) <= lim), np.max(np.abs(got - ref) / lim)
+
+
+def test_w4_tiny_rows_next_to_others():
+    """A row of 1e-37 among rows of zeros, of 1e30, of NaN and infinities, under weights large enough that its
+    outputs are normal numbers: held to its own size."""
+    r = rng_for(78)
+    G, K, dg = 2, 128, 70
+    codes, scales = make_w4(r, G, dg, K)
+    scales = (scales + 90).astype(np.uint8)
+    x = r.standard_normal((8, G * K))
+    x[0] = 0
+    x[1] *= 1e-37
+    x[2] *= 1e-30
+    x[3, 3], x[4, K + 9] = np.nan, np.inf
+    x[5] *= 1e-20
+    xt = gpu(x, BF16)
+    got = run_w4(xt, None, codes, scales, G, K, dg, F32)
+    x64 = np.where(np.isfinite(np64(xt)), np64(xt), 0)
+    ref, mag, top = w4_reference(x64, codes, scales, G, K, dg)
+    ok = np.abs(got - ref) <= (K + 1) * 2.0 ** -24 * mag + SPLIT * top
+    assert np.isnan(got[3, :dg]).all() and np.isnan(got[4, dg:]).all()
+    ok[3, :dg] = ok[4, dg:] = True
+    assert ok.all() and np.abs(got[1]).max() > 1e-10 and not got[0].any()
