@@ -474,11 +474,13 @@ lc_status lc_grouped_out_proj(const lc_out_proj_args* a, void* stream);
  *
  * add_rms_norm — the residual's addition and RMSNorm with a weight:
  *   r = x + res (res NULL: r = x);  res_out = r;  y = r / sqrt(mean(r^2) + eps) * w.
- * r and the sum of squares are FP32; res_out is r rounded to in_fmt, y comes from the
- * unrounded r.  out_fmt LC_FMT_MXFP8 writes E4M3 codes and, per 32 consecutive values, the
- * E8M0 scale X (byte e + 127, X = 2^e): the smallest power of two with max |y| <= 448 X over
- * the block's finite values (e clamped to [-127, 127]; a block of zeros takes 2^0), so no
- * finite value saturates; infinities become +-448 X, NaN the E4M3 NaN.
+ * r, the sum of squares and r w (formed before the root's factor) are FP32, and have to stay in its
+ * range: a row whose squares sum to more than that gives y = 0, and with eps = 0 one whose squares
+ * are all below it gives infinities or NaN.  res_out is r rounded to in_fmt, y comes from the
+ * unrounded r.  out_fmt LC_FMT_MXFP8 writes E4M3 codes and, per 32 consecutive values, the E8M0
+ * scale X (byte e + 127, X = 2^e): the smallest power of two with max |y| <= 448 X over the block's
+ * finite values (e clamped to [-127, 127]; a block of zeros takes 2^0), so no finite value
+ * saturates; infinities become +-448 X, NaN the E4M3 NaN.
  * res_out may be res or x itself (in place); any other overlap of inputs and outputs is not
  * allowed.
  * ------------------------------------------------------------------------------- */
@@ -510,8 +512,9 @@ lc_status lc_add_rms_norm(const lc_add_rms_norm_args* a, void* stream);
  * BF16 row is split there into two E4M3 terms, exact for values of at least 1 / 14336 (2^-13.8)
  * of the largest of their 32-value block and within 2^-21.8 of that largest value below.  A NaN
  * or an infinity in a BF16 row makes the row's outputs of that group NaN.  Each 32 rows of BF16
- * x (64 of MXFP8) read the weights once: for many rows use a 16-bit product instead.  Up to 65535
- * times as many rows; G K up to 2^30; fewer than 2^24 tiles of 128 outputs.
+ * x (64 of MXFP8) read the weights again; for the rows of a prompt a BF16 product of weights that
+ * the caller has widened (grouped_out_proj) reads them once.  Up to 65535 times as many rows;
+ * G K up to 2^30; fewer than 2^24 tiles of 128 outputs.
  * ------------------------------------------------------------------------------- */
 typedef struct lc_w4_proj_args {
   int32_t n_q;             /* rows of x */
@@ -585,8 +588,12 @@ lc_status lc_kv8_append(const lc_kv8_append_args* a, void* stream);
  *   l_t = scale <q_h, k_t>, M = max(sink_h, max l), Z = e^(sink_h - M) + sum e^(l_t - M),
  *   o = sum e^(l_t - M) v_t / Z, lse = M + ln Z   (sink NULL: no sink term).
  * A query that sees no token gets o = 0 and lse = sink_h (-inf without a sink).  out and lse
- * rows past q_start[num_seqs] are left as they were.  A NaN among the keys or values a query
- * sees makes its outputs NaN; what it does not see never reaches it.
+ * rows past q_start[num_seqs] are left as they were.  A NaN among the keys a query sees makes its
+ * outputs NaN, one among its values the output of that dim; what it does not see never reaches it.
+ * Logits, M, Z and the sums are FP32.  The weights that multiply the values are rounded to F16 (11
+ * bits) under the largest of them, Z is summed before that; a query's dims are exact down to 2^-39
+ * of its largest one.  Over random caches that makes 1.5e-4 of o (2-norm), a tenth of its rounding
+ * to BF16.
  * Prefill: any number of queries per sequence.  Decode: one query per sequence (n_q ==
  * num_seqs, q_start[s] = s).  Both split the keys over CTAs where there are few rows, and then
  * need a workspace of lc_kv8_attn_workspace_bytes(a, decode) bytes (host fields only; it holds

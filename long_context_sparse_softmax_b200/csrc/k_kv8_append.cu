@@ -5,8 +5,9 @@
 // registers, as they came, between the maximum and the rounding, so they are read once.  Memory's
 // latency bounds it (a CTA lives for a few accesses), so the rows are fetched before the block's id
 // is known, and little is held per thread: six CTAs on a multiprocessor.  16384 BF16 tokens of 8 heads of
-// 128 dims: 18.5 us, 5.4 TB/s (84 % of the measured copy rate; 38.9 us with the id first and wide
-// divisions); a token for each of 32 sequences 3.1 us, a launch and three latencies.  The scale is the
+// 128 dims: 18.9 us in a graph of such calls, 5.3 TB/s (82 % of the measured copy rate), 20.7 us as a call among
+// others (38.9 us with the id first and wide divisions); a token for each of 32 sequences 3.2 us in a graph, 5.8 as
+// a call: a launch and three latencies.  The scale is the
 // smallest 2^e that covers them (exact integer arithmetic on the exponent), kept at or above the
 // scale of a block that already holds tokens; where that grows, the block's older codes are
 // rounded again from their exact values.  Everything is exact but the final roundings, so the

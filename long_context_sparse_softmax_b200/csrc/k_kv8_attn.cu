@@ -14,16 +14,19 @@
 //
 // Queries are scaled per row by a power of two into F16's range (exact down to 2^-39 of the row's
 // largest value); K's block scale multiplies the logits, V's joins the softmax exponent (see
-// lc_kv8.cuh).  P is rounded to F16 (11 bits); l sums the unrounded weights.  The reference R moves
+// lc_kv8.cuh).  P is rounded to F16 (11 bits), the operand that the codes widen to exactly; l sums the
+// unrounded weights.  That rounding is 1.4e-4 of o (2-norm), a tenth of o's own to BF16 (1.65e-3 with it or
+// without); a second F16 term for the rest of P would double the products with V.  The reference R moves
 // only when a weight would pass 2^8, so the lanes meet once per 16 keys, in a vote.
 //
 // Warps of a CTA take 16-key steps in turn and join through shared memory; the keys of a row
 // tile are split over CTAs, joined by k_kv8_combine.
 //
 // HBM bounds it: a step of a warp is 4 KB (128 dims).  One context of 262144 tokens, 8 shared heads, 64
-// queries' heads: 96 us, 5.6 TB/s (86 % of the measured copy rate; the join is 5 us of it).  32 contexts up
-// to 16384: 100 us, 5.5 TB/s (86 %): here a CTA has 16 steps a warp, and what it does besides (about 1100
-// instructions a warp, one after another) costs as much as 100 keys; the join is 5 us.  What brought it there:
+// queries' heads: 95 us, 5.7 TB/s (87 % of the measured copy rate; the join is 5 us of it).  32 contexts up
+// to 16384: 100 us in a graph of such calls, 5.6 TB/s (86 %), 111 us as a call among others (78 %): here a
+// CTA has 16 steps a warp, and what it does besides (about 1100 instructions a warp, one after another) costs
+// as much as 100 keys; the join is 5 us.  What brought it there:
 // two conversions per instruction pair and no divisions by the block size (209 -> 157 us for the batch),
 // block ids before the queries, 32-bit index arithmetic (143), splits of 1024 keys (127), the ring (119 -> 106:
 // loads of 16 bytes a lane straight into registers kept L1 75 % busy, 99 % for one context; that one lost 94 ->
@@ -614,6 +617,8 @@ namespace {
 // Measured (us, k_kv8_attn / k_kv8_attn_tc), 8 heads of 128 dims, 8 query heads each: one sequence of 8192
 // tokens 16.5 / 17.3 at 16 rows, 19.9 / 18.1 at 32, 32 / 19 at 64; of 65536 49 / 68, 87 / 66, 161 / 70; eight of
 // 8192 35 / 70, 63 / 71, 116 / 74.  8 heads of 64 dims, 4 query heads each, eight of 8192: 48 / 44 at 32, 66 / 46 at 64.
+// The rule looks at the rows of one sequence alone: for several sequences of 32 rows (four queries, 8 heads
+// each) it takes the slower kernel, by an eighth in the table above.
 constexpr int kTcRows = 32;
 
 // Splits that any row tile of the call can have.

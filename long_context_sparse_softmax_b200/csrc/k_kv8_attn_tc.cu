@@ -5,7 +5,7 @@
 // head r % g of the group), which share every key tile of 128 tokens:
 //   S_i = Q_i K^T   M = 128 rows, N = 64 keys (half tiles, two of them per row tile), both K-major in
 //                   shared memory;
-//   P_i             F16 weights, written over S_i's columns of tensor memory;
+//   P_i             F16 weights (11 bits: see k_kv8_attn.cu), written over S_i's columns of tensor memory;
 //   O_i += P_i V    A = P_i in tensor memory, B = V (keys x dims, dims contiguous: MN-major).
 // The codes are widened to F16 (exact) once per CTA, and the row's softmax keeps the precision that
 // it has with few rows.  S of a half tile is computed while the softmax works on the half before, and
@@ -22,8 +22,9 @@
 // What bounds it: the exponentials (16 a cycle on a multiprocessor: 2048 cycles per 256 x 128 tile, as
 // many as its products take) and the latency of each softmax step; a tile takes about 4000 cycles, 2950
 // of them for the weights.
-// 2048 queries at the end of 8192 tokens, 64 / 8 heads of 128 dims: 498 us, 965 TFLOP/s (57 % of the
-// measured F16 rate; 512 CTAs are 3.46 rounds of 148, run as 4).  On the way there: a mma.sync kernel with
+// 2048 queries at the end of 8192 tokens, 64 / 8 heads of 128 dims: 501 us in a graph of such calls, 960
+// TFLOP/s (56 % of the measured F16 rate; 512 CTAs are 3.46 rounds of 148, run as 4), 521 us as a call among
+// others.  On the way there: a mma.sync kernel with
 // 8 rows a tile 4960 us; 256 rows on tcgen05 1190; packed FP32 pairs and a uniform issuing warp 734; half
 // tiles ahead of the softmax 545; cheaper widening and masks 520.
 #include "lc_e4m3.cuh"

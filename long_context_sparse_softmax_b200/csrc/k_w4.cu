@@ -25,11 +25,13 @@
 // (LC_DEV_TIMEOUT).
 //
 // What bounds it is the chain through these roles, not memory: one row through 7168 x 4096 takes
-// 9.1 us in a graph (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.5 us for 14
+// 9.1 us in a graph, 8.2 as a call among others (2.4 us of weights at 6.47 TB/s): 2 us to the first full stage, 3.5 us for 14
 // steps (scales -> MMAs -> stage free), 1.4 us to join 4 CTAs, the rest is the start of the next
 // cluster.  32 rows through 8 groups of 4096 x 1024: 14.9 us, of which widening x (16 conversions per
 // 8 values, in every CTA that shares them) took 850 cycles a step when the whole took 15.3; 17 rows of MXFP8 through
 // 7168 x 7000: 14.3 us.
+// The rows of a prompt read and lay out the weights for every 32 (64 of MXFP8) of them: 2048 rows through
+// 7168 x 4096 take 446 us (200), 270 TFLOP/s (600).
 // Tried: cp.async in place of the bulk copies (50 cycles of issue each: 12.7 and 18.4 us), one x
 // block per thread (1000 cycles a step), two steps per round of the issuing warps (11.0 and 16.7, when
 // this took 10.7 and 16.4), BF16 weights by table lookup for the warps' own matrix instruction (9.5 us
