@@ -19,7 +19,7 @@
 // An MXFP8 block is 4 neighbouring lanes' values (two shuffles for its maximum).
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
-#include "lc_ptx.cuh"
+#include "lc_ptx_dense.cuh"
 
 namespace lc {
 

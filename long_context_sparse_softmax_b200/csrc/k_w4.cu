@@ -42,7 +42,7 @@
 
 #include "lc_e4m3.cuh"
 #include "lc_internal.h"
-#include "lc_ptx.cuh"
+#include "lc_ptx_dense.cuh"
 #include "lc_tma.h"
 
 namespace lc {

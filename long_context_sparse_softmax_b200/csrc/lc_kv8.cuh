@@ -10,7 +10,7 @@
 #pragma once
 
 #include "lc_internal.h"
-#include "lc_ptx.cuh"
+#include "lc_ptx_dense.cuh"
 
 namespace lc {
 

@@ -71,14 +71,6 @@ __device__ __forceinline__ void tma_tile2d(uint32_t dst, const CUtensorMap* map,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// the same of a 3-D tensor
-__device__ __forceinline__ void tma_tile3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::
-          "r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
-}
 // four rows r0..r3 (one-row box) of a 2-D tensor, starting at column x
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
                                             uint32_t bar) {
@@ -136,13 +128,6 @@ __device__ __forceinline__ uint32_t sw128_off(int r, int j) { return r * 128 + (
 __device__ __forceinline__ uint32_t sw64_off(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
 
 // ---------------------------------------------------------------- tcgen05 MMAs
-// true in one lane of the (converged) warp; a branch on it leaves the other registers warp-uniform
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
-}
-
 // D (tensor memory) = A * B (+ D if acc): kind::f16 (BF16 / F16 operands)
 __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -208,48 +193,6 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // pdl_trigger() lets the kernel after this one start early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
-// ---------------------------------------------------------------- arithmetic
-// the larger of each pair of 16-bit numbers
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// pairs of FP32 values (one instruction for two products or sums)
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1,%2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2_regs(uint32_t& x, uint32_t& y, uint64_t m, uint64_t c) {
-  asm("{\n.reg .b64 t;\nmov.b64 t, {%0,%1};\nfma.rn.f32x2 t, t, %2, %3;\nmov.b64 {%0,%1}, t;\n}\n" : "+r"(x), "+r"(y) : "l"(m), "l"(c));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t a) {
-  float2 v;
-  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(v.x), "=f"(v.y) : "l"(a));
-  return v;
-}
-__device__ __forceinline__ float sum2(uint64_t a) {
-  float x, y;
-  asm("mov.b64 {%0,%1}, %2;\n" : "=f"(x), "=f"(y) : "l"(a));
-  return x + y;
-}
 
 // 2^x (approximate, flush-to-zero), the softmax exponent
 __device__ __forceinline__ float ex2(float x) {
